@@ -432,6 +432,112 @@ PACT_API pact_status pact_rmsnorm_bwd(const pact_bf16 *dy, int64_t lddy, const p
                              const pact_bf16 *dres, pact_bf16 *dx, const pact_nvfp4_t *dxq,
                              pact_stream_t stream);
 
+/* ------------------------------------- A11: rotation of queries and keys */
+/* Beside the pages (they leave the attention core out): the position rotation of the
+ * decoder layers this data flow serves.  For each row at position p = positions[row]
+ * and the pair (a, b) = (x[i], x[i + head_dim/2]) of each of `heads` heads side by side:
+ *   y[i] = a cos t - b sin t,  y[i + head_dim/2] = b cos t + a sin t,  t = p inv_freq[i]
+ * in FP32 with t reduced in FP64 (far positions keep their angle), rounded once to
+ * BF16.  inverse != 0 rotates by -t: the gradient (the transpose) of the rotation.
+ * x [M x heads*head_dim] (row stride ldx; e.g. the q and k columns of a q|k|v output),
+ * y likewise (row stride ldy); y may be x itself with the same stride, and otherwise
+ * must not overlap it.  positions: M int32; a negative one marks a row of padding,
+ * which is not written.  inv_freq: HOST array of head_dim/2 doubles, read before the
+ * call returns.  head_dim is 64 or 128. */
+PACT_API pact_status pact_rope(const pact_bf16 *x, int64_t ldx, int64_t M, int heads, int head_dim,
+                               const int32_t *positions, const double *inv_freq, int inverse, pact_bf16 *y,
+                               int64_t ldy, pact_stream_t stream);
+
+/* ------------------------------------------ A12: packed causal attention */
+/* The attention core between the q|k|v and o projections (beside the pages, which take
+ * its output as given): causal softmax attention over packed sequences with grouped
+ * heads.  Sequence s owns rows [seq_start[s], seq_start[s+1]) of q, k and v; query head
+ * h reads key head h / (heads / kv_heads).  For row i of a sequence, over its rows j <= i:
+ *   S_ij = scale q_i . k_j,  lse_i = log sum_j exp S_ij,  o_i = sum_j exp(S_ij - lse_i) v_j
+ * Scores, softmax statistics and sums are FP32; the probabilities enter the second
+ * product as BF16 (as q, k and v do), o is rounded once to BF16. */
+typedef struct {
+    int64_t M;                 /* rows of q, k, v and the outputs (1 .. 2^30) */
+    int heads, kv_heads;       /* heads a multiple of kv_heads */
+    int head_dim;              /* 64 or 128 */
+    float scale;               /* of the scores, usually head_dim^-1/2 */
+    const pact_bf16 *q;        /* [M x heads*head_dim], row stride ldq */
+    int64_t ldq;
+    const pact_bf16 *k;        /* [M x kv_heads*head_dim], row stride ldk */
+    int64_t ldk;
+    const pact_bf16 *v;        /* [M x kv_heads*head_dim], row stride ldv */
+    int64_t ldv;
+    const int32_t *seq_start;  /* device, nseq + 1 non-decreasing row numbers in [0, M]; a
+                                  sequence may be empty */
+    int nseq;                  /* 1 .. 2^20 */
+} pact_attention_t;
+
+/* o [M x heads*head_dim] (row stride ldo) and lse [heads x M] FP32 (natural logarithm,
+ * for the gradient).  Rows of no sequence are left as they were.  A row's result does
+ * not depend on other sequences or on rows of none, whatever they hold; a value that is
+ * not finite may reach every row of its own sequence.  seq_start is read on the device:
+ * numbers outside [0, M] are taken as the nearest end, and where they decrease the rows
+ * concerned are unspecified (no access leaves the M rows).  Outputs must not overlap
+ * the inputs. */
+PACT_API pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o, int64_t ldo, float *lse,
+                                        pact_stream_t stream);
+
+/* Gradient of pact_attention_fwd.  With P_ij = exp(S_ij - lse_i), delta_i = do_i . o_i
+ * and dS_ij = P_ij (do_i . v_j - delta_i):
+ *   dq_i = scale sum_j dS_ij k_j;  dk_j = scale sum dS_ij q_i,  dv_j = sum P_ij do_i  over
+ *   the rows i and the query heads of j's group.
+ * P and dS enter their products as BF16; every sum is FP32 in a fixed order (repeated
+ * calls agree bit for bit).  Rows of no sequence are left as they were.  workspace
+ * (device, 16-byte aligned, >= pact_attention_bwd_workspace_bytes(M, heads)) is scratch;
+ * calls that share it must not overlap on the GPU. */
+typedef struct {
+    const pact_bf16 *o;        /* [M x heads*head_dim] as written by the forward */
+    int64_t ldo;
+    const float *lse;          /* [heads x M] as written by the forward */
+    const pact_bf16 *dout;     /* [M x heads*head_dim], the gradient of o */
+    int64_t lddout;
+    pact_bf16 *dq;             /* out, shaped as q, k, v */
+    int64_t lddq;
+    pact_bf16 *dk;
+    int64_t lddk;
+    pact_bf16 *dv;
+    int64_t lddv;
+} pact_attention_grad_t;
+PACT_API size_t pact_attention_bwd_workspace_bytes(int64_t M, int heads);
+PACT_API pact_status pact_attention_bwd(const pact_attention_t *a, const pact_attention_grad_t *g, void *workspace,
+                                        size_t ws_bytes, pact_stream_t stream);
+
+/* ------------------------------------------------ A13: the adapters' update */
+/* Beside the pages: the update of the LoRA matrices by an orthogonalised momentum (the
+ * Muon optimiser's Newton-Schulz products; K. Jordan et al., 2024), for many skinny
+ * matrices in one call.  For each, with r = min(rows, cols):
+ *   m' = momentum m + g;  u = g + momentum m' (nesterov != 0) or m'
+ *   X = u / (|u|_F + 1e-7);  five times, on the side of the r rows:
+ *       A = X X^T,  X <- 3.4445 X + (-4.7750 A + 2.0315 A^2) X
+ *   W' = (1 - lr weight_decay) W - lr sqrt(max(1, rows / cols)) X
+ * m and W are FP32 (a BF16 weight would lose small steps); W' is also written rounded
+ * to BF16 where weight_bf16 is not NULL, the adapter the LoRA products read.  Gradients
+ * are BF16, or FP32 when grad_fp32 != 0 (pact_lora_bwd's two forms).  The r x r products
+ * run in FP64. */
+typedef struct {
+    const void *grad;          /* [rows x cols], contiguous, as are all below */
+    const float *momentum;     /* m */
+    float *momentum_out;       /* m'; may be momentum itself */
+    const float *weight;       /* W */
+    float *weight_out;         /* W'; may be weight itself */
+    pact_bf16 *weight_bf16;    /* BF16_RNE(W') or NULL */
+    int64_t rows, cols;        /* the shorter at most 64, the longer at most 2^24 */
+} pact_muon_matrix_t;
+/* mats: HOST array of n matrices, read before the call returns; pointers aligned to
+ * their elements (16-byte aligned ones with cols a multiple of 4 are read faster).
+ * Matrices must not overlap one another.  workspace: device, 16-byte aligned, >=
+ * pact_muon_workspace_bytes(mats, n) (which reads rows and cols only); calls that share
+ * it must not overlap on the GPU. */
+PACT_API size_t pact_muon_workspace_bytes(const pact_muon_matrix_t *mats, int n);
+PACT_API pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32, double lr,
+                                    double momentum, double weight_decay, int nesterov, void *workspace,
+                                    size_t ws_bytes, pact_stream_t stream);
+
 /* ------------------------------------------------------------ status */
 /* Message of the last failing call on this thread ("" if none). */
 PACT_API const char *pact_last_error(void);

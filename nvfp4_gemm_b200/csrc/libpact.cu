@@ -5,3 +5,6 @@
 #include "gemm.cu"
 #include "lora.cu"
 #include "gptq.cu"
+#include "rope.cu"
+#include "attn.cu"
+#include "muon.cu"

@@ -54,6 +54,27 @@ class c_lora_bwd(ctypes.Structure):
                 ("dB", ctypes.c_void_p), ("grads_fp32", ctypes.c_int)]
 
 
+class c_attention(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q", ctypes.c_void_p), ("ldq", ctypes.c_int64), ("k", ctypes.c_void_p), ("ldk", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("ldv", ctypes.c_int64),
+                ("seq_start", ctypes.c_void_p), ("nseq", ctypes.c_int)]
+
+
+class c_attention_grad(ctypes.Structure):
+    _fields_ = [("o", ctypes.c_void_p), ("ldo", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("dout", ctypes.c_void_p), ("lddout", ctypes.c_int64),
+                ("dq", ctypes.c_void_p), ("lddq", ctypes.c_int64), ("dk", ctypes.c_void_p), ("lddk", ctypes.c_int64),
+                ("dv", ctypes.c_void_p), ("lddv", ctypes.c_int64)]
+
+
+class c_muon_matrix(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p), ("momentum_out", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("weight_out", ctypes.c_void_p), ("weight_bf16", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"libpact.so is not built ({LIB_PATH}); run nvfp4_gemm_b200/build.py")
@@ -96,6 +117,14 @@ def _load() -> ctypes.CDLL:
         "pact_lora_bwd": (S, [ctypes.POINTER(c_lora_bwd), P, ctypes.c_size_t, P]),
         "pact_silu_mul_bwd_quant": (S, [P, I64, NV, NV, I64, I64, P, I64, NV, P, P]),
         "pact_rmsnorm_bwd": (S, [P, I64, NV, P, P, I64, I64, P, P, NV, P]),
+        "pact_rope": (S, [P, I64, I64, I, I, P, ctypes.POINTER(ctypes.c_double), I, P, I64, P]),
+        "pact_attention_fwd": (S, [ctypes.POINTER(c_attention), P, I64, P, P]),
+        "pact_attention_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I]),
+        "pact_attention_bwd": (S, [ctypes.POINTER(c_attention), ctypes.POINTER(c_attention_grad), P, ctypes.c_size_t,
+                                   P]),
+        "pact_muon_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(c_muon_matrix), I]),
+        "pact_muon_step": (S, [ctypes.POINTER(c_muon_matrix), I, I, ctypes.c_double, ctypes.c_double,
+                               ctypes.c_double, I, P, ctypes.c_size_t, P]),
         "pact_last_error": (ctypes.c_char_p, []),
         "pact_status_string": (ctypes.c_char_p, [S]),
         "pact_get_device_status": (S, [P]),
@@ -588,6 +617,177 @@ def pact_rmsnorm_bwd(dy: torch.Tensor, yq: NVFP4Tensor, rstd: torch.Tensor, gamm
     _check(_lib.pact_rmsnorm_bwd(dy.data_ptr(), _ld(dy), ctypes.byref(sy), rstd.data_ptr(), gamma.data_ptr(), M, H,
                                  _ptr(dres), dx.data_ptr(), ctypes.byref(sq) if sq else None, _stream(stream)))
     return dx, dxq
+
+
+def _on(t: torch.Tensor, name: str, dtype, shape=None) -> torch.Tensor:
+    """t is a tensor of this type and shape on the current device (where the call launches)."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA {str(dtype).replace('torch.', '')} tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {list(t.shape)}, expected {list(shape)}")
+    return t
+
+
+def _matrix(t: torch.Tensor, name: str, shape=None) -> int:
+    """The row stride of a BF16 matrix (of this shape) with contiguous rows."""
+    _on(t, name, torch.bfloat16, shape)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: expected a matrix with contiguous rows")
+    # a single row's stride is arbitrary in PyTorch: any legal one serves
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor a call allocates for itself.  Its memory belongs to the current stream; where the call runs on
+    another one, the allocator is told, so that freeing it does not hand it out while that stream still uses it."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+    return t
+
+
+def pact_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: Sequence[float], heads: int,
+              y: Optional[torch.Tensor] = None, inverse: bool = False, stream=None) -> torch.Tensor:
+    """Rotate `heads` heads side by side in x [M x heads * head_dim] (row stride free, e.g. the q|k columns of
+    a q|k|v output) by their rows' positions (int32 [M], negative: padding, not written).  inv_freq: the
+    head_dim / 2 angles per position, host values.  y may be x (in place); inverse gives the gradient."""
+    ldx = _matrix(x, "x")
+    M, cols = x.shape
+    if heads < 1 or cols % heads:
+        raise ValueError(f"x: {cols} columns do not divide into {heads} heads")
+    _on(positions, "positions", torch.int32, (M,))
+    if positions.stride(0) != 1 and M > 1:
+        raise ValueError("positions: expected a contiguous vector")
+    freq = [float(f) for f in (inv_freq.tolist() if hasattr(inv_freq, "tolist") else inv_freq)]
+    if len(freq) != cols // heads // 2:
+        raise ValueError(f"inv_freq: {len(freq)} values, expected {cols // heads // 2}")
+    if y is None:
+        y = _new((M, cols), torch.bfloat16, x.device, stream)
+    ldy = _matrix(y, "y", (M, cols))
+    _check(_lib.pact_rope(x.data_ptr(), ldx, M, heads, cols // heads, positions.data_ptr(),
+                          (ctypes.c_double * len(freq))(*freq), int(bool(inverse)), y.data_ptr(), ldy,
+                          _stream(stream)))
+    return y
+
+
+def _attention(q, k, v, seq_start, heads, kv_heads, scale) -> c_attention:
+    ldq, ldk, ldv = _matrix(q, "q"), _matrix(k, "k"), _matrix(v, "v")
+    M = q.shape[0]
+    if heads < 1 or kv_heads < 1 or q.shape[1] % heads:
+        raise ValueError(f"q: {q.shape[1]} columns do not divide into {heads} heads")
+    D = q.shape[1] // heads
+    for t, name in ((k, "k"), (v, "v")):
+        _on(t, name, torch.bfloat16, (M, kv_heads * D))
+    _on(seq_start, "seq_start", torch.int32)
+    if seq_start.dim() != 1 or seq_start.numel() < 2 or seq_start.stride(0) != 1:
+        raise ValueError("seq_start: expected a contiguous vector of at least two row numbers")
+    return c_attention(M, heads, kv_heads, D, D ** -0.5 if scale is None else float(scale), q.data_ptr(), ldq,
+                       k.data_ptr(), ldk, v.data_ptr(), ldv, seq_start.data_ptr(), seq_start.numel() - 1)
+
+
+def _lse(t: torch.Tensor, shape) -> torch.Tensor:
+    _on(t, "lse", torch.float32, shape)
+    if not t.is_contiguous():
+        raise ValueError("lse: expected a contiguous tensor")
+    return t
+
+
+def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_start: torch.Tensor, heads: int,
+                       kv_heads: int, scale: Optional[float] = None, o: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over packed sequences: q [M x heads * D], k, v [M x kv_heads * D] (row strides free),
+    seq_start int32 [sequences + 1] on the device.  Returns o [M x heads * D] and lse [heads x M]; rows of no
+    sequence are not written.  scale defaults to D ** -0.5."""
+    a = _attention(q, k, v, seq_start, heads, kv_heads, scale)
+    if o is None:
+        o = _new(q.shape, torch.bfloat16, q.device, stream)
+    if lse is None:
+        lse = _new((heads, a.M), torch.float32, q.device, stream)
+    ldo = _matrix(o, "o", q.shape)
+    _check(_lib.pact_attention_fwd(ctypes.byref(a), o.data_ptr(), ldo, _lse(lse, (heads, a.M)).data_ptr(),
+                                   _stream(stream)))
+    return o, lse
+
+
+def pact_attention_bwd_workspace_bytes(M: int, heads: int) -> int:
+    return int(_lib.pact_attention_bwd_workspace_bytes(M, heads))
+
+
+def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                       lse: torch.Tensor, seq_start: torch.Tensor, heads: int, kv_heads: int,
+                       scale: Optional[float] = None, dq: Optional[torch.Tensor] = None,
+                       dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None):
+    """dq, dk, dv of pact_attention_fwd from the gradient do of its output; o and lse are what it wrote."""
+    a = _attention(q, k, v, seq_start, heads, kv_heads, scale)
+    new = lambda t: _new(t.shape, torch.bfloat16, q.device, stream)  # noqa: E731
+    dq, dk, dv = dq if dq is not None else new(q), dk if dk is not None else new(k), dv if dv is not None else new(v)
+    g = c_attention_grad(o.data_ptr(), _matrix(o, "o", q.shape), _lse(lse, (heads, a.M)).data_ptr(), do.data_ptr(),
+                         _matrix(do, "do", q.shape), dq.data_ptr(), _matrix(dq, "dq", q.shape), dk.data_ptr(),
+                         _matrix(dk, "dk", k.shape), dv.data_ptr(), _matrix(dv, "dv", v.shape))
+    ws = workspace
+    if ws is None:
+        ws = _new(pact_attention_bwd_workspace_bytes(a.M, heads), torch.uint8, q.device, stream)
+    _check(_lib.pact_attention_bwd(ctypes.byref(a), ctypes.byref(g), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                   _stream(stream)))
+    return dq, dk, dv
+
+
+def _muon_matrices(weights, grads, momenta, weights_out, momenta_out, weights_bf16):
+    """The pact_muon_matrix_t array of lists of contiguous tensors [rows x cols] or [count x rows x cols]."""
+    n = len(weights)
+    cols = (weights, grads, momenta, weights_out, momenta_out)
+    if n == 0 or any(len(c) != n for c in cols) or (weights_bf16 is not None and len(weights_bf16) != n):
+        raise ValueError("expected one entry per weight in every list, and at least one weight")
+    gdt = grads[0].dtype
+    if gdt not in (torch.float32, torch.bfloat16):
+        raise TypeError("grads: expected bfloat16 or float32 tensors")
+    mats = []
+    for i, w in enumerate(weights):
+        if w.dim() not in (2, 3) or w.numel() == 0:
+            raise ValueError(f"weights[{i}]: expected a matrix or a batch of matrices")
+        w16 = weights_bf16[i] if weights_bf16 is not None else None
+        parts = [("grads", grads[i], gdt), ("momenta", momenta[i], torch.float32),
+                 ("momenta_out", momenta_out[i], torch.float32), ("weights", w, torch.float32),
+                 ("weights_out", weights_out[i], torch.float32), ("weights_bf16", w16, torch.bfloat16)]
+        for name, t, dt in parts:
+            if t is None:
+                continue
+            _on(t, f"{name}[{i}]", dt, w.shape)
+            if not t.is_contiguous():
+                raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
+        rows, k = w.shape[-2:]
+        at = [(t.data_ptr(), rows * k * t.element_size()) if t is not None else (0, 0) for _, t, _ in parts]
+        mats += [c_muon_matrix(*(p + j * step if p else None for p, step in at), rows, k)
+                 for j in range(w.numel() // (rows * k))]
+    return (c_muon_matrix * len(mats))(*mats), gdt == torch.float32
+
+
+def pact_muon_step(weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], momenta: Sequence[torch.Tensor],
+                   lr: float, momentum: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True,
+                   weights_out: Optional[Sequence[torch.Tensor]] = None,
+                   momenta_out: Optional[Sequence[torch.Tensor]] = None,
+                   weights_bf16: Optional[Sequence[torch.Tensor]] = None,
+                   workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One orthogonalised-momentum step of many skinny matrices (the shorter side at most 64): contiguous FP32
+    weights and momenta and BF16 or FP32 grads, [rows x cols] or [count x rows x cols] each.  In place unless
+    weights_out / momenta_out are given; weights_bf16 receive the BF16 copies."""
+    mats, fp32 = _muon_matrices(weights, grads, momenta, weights_out if weights_out is not None else weights,
+                                momenta_out if momenta_out is not None else momenta, weights_bf16)
+    ws = workspace
+    if ws is None:
+        ws = _new(int(_lib.pact_muon_workspace_bytes(mats, len(mats))), torch.uint8, weights[0].device, stream)
+    _check(_lib.pact_muon_step(mats, len(mats), int(fp32), float(lr), float(momentum), float(weight_decay),
+                               int(bool(nesterov)), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def pact_muon_workspace_bytes(shapes: Sequence[Sequence[int]]) -> int:
+    """Scratch bytes of a pact_muon_step over matrices of these (rows, cols)."""
+    mats = (c_muon_matrix * len(shapes))(*(c_muon_matrix(None, None, None, None, None, None, r, c)
+                                           for r, c in shapes))
+    return int(_lib.pact_muon_workspace_bytes(mats, len(mats)))
 
 
 def pact_get_device_status(stream=None) -> int:

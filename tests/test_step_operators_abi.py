@@ -1,0 +1,103 @@
+"""Refusals of the rotation, attention and update calls, without a GPU: the library's host checks
+(nothing is enqueued) and the binding's."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def P():
+    import importlib.util
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("_pact_build", os.path.join(root, "nvfp4_gemm_b200", "build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    b.build()
+    import nvfp4_gemm_b200 as p
+    return p
+
+
+INVALID, SHAPE, ALIGN = 1, 2, 3
+
+
+def test_rope(P):
+    freq = (ctypes.c_double * 64)()
+    call = lambda x=0x1000, ldx=512, M=4, h=4, D=128, pos=0x2000, f=freq, y=0x3000, ldy=512: P.pact.lib.pact_rope(
+        x, ldx, M, h, D, pos, f, 0, y, ldy, None)
+    assert call(x=None) == call(pos=None) == call(y=None) == call(f=None) == INVALID
+    assert call(D=96) == call(M=0) == call(h=0) == call(ldx=504) == call(ldy=504) == call(M=2 ** 31) == SHAPE
+    assert call(x=0x1008) == call(y=0x3004) == call(ldx=516) == call(pos=0x2002) == ALIGN
+    assert "aligned" in P.pact_last_error()
+
+
+def attention(P, **kw):
+    a = P.pact.c_attention(300, 8, 2, 64, 0.125, 0x1000, 512, 0x2000, 128, 0x3000, 128, 0x4000, 3)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return ctypes.byref(a)
+
+
+BAD = [(dict(q=None), INVALID), (dict(seq_start=None), INVALID), (dict(scale=float("nan")), INVALID),
+       (dict(head_dim=96), SHAPE), (dict(heads=7), SHAPE), (dict(heads=0), SHAPE), (dict(kv_heads=0), SHAPE),
+       (dict(M=0), SHAPE), (dict(M=2 ** 30 + 1), SHAPE), (dict(nseq=0), SHAPE), (dict(ldq=504), SHAPE),
+       (dict(ldk=120), SHAPE), (dict(ldv=120), SHAPE), (dict(q=0x1008), ALIGN), (dict(k=0x2002), ALIGN),
+       (dict(v=0x3008), ALIGN), (dict(ldv=132), ALIGN), (dict(seq_start=0x4002), ALIGN)]
+
+
+@pytest.mark.parametrize("kw,status", BAD, ids=lambda x: str(x))
+def test_attention_arguments(P, kw, status):
+    lib = P.pact.lib
+    assert lib.pact_attention_fwd(attention(P, **kw), 0x5000, 512, 0x6000, None) == status
+    g = P.pact.c_attention_grad(0x5000, 512, 0x6000, 0x7000, 512, 0x8000, 512, 0x9000, 128, 0xA000, 128)
+    assert lib.pact_attention_bwd(attention(P, **kw), ctypes.byref(g), 0xB000, 1 << 30, None) == status
+
+
+def test_attention_outputs(P):
+    lib = P.pact.lib
+    assert lib.pact_attention_fwd(None, 0x5000, 512, 0x6000, None) == INVALID
+    assert lib.pact_attention_fwd(attention(P), None, 512, 0x6000, None) == INVALID
+    assert lib.pact_attention_fwd(attention(P), 0x5000, 504, 0x6000, None) == ALIGN
+    assert lib.pact_attention_fwd(attention(P), 0x5000, 512, 0x6004, None) == ALIGN
+    need = P.pact_attention_bwd_workspace_bytes(300, 8)
+    assert need > 0 and P.pact_attention_bwd_workspace_bytes(0, 8) == 0
+    names = [f[0] for f in P.pact.c_attention_grad._fields_]
+    good = (0x5000, 512, 0x6000, 0x7000, 512, 0x8000, 512, 0x9000, 128, 0xA000, 128)
+    call = lambda ws=0xB000, n=need, **kw: lib.pact_attention_bwd(
+        attention(P), ctypes.byref(P.pact.c_attention_grad(*[kw.get(k, v) for k, v in zip(names, good)])), ws, n, None)
+    for name in ("o", "lse", "dout", "dq", "dk", "dv"):
+        assert call(**{name: None}) == INVALID
+        assert call(**{name: 0x5008}) == ALIGN
+    assert call(ws=None) == call(n=need - 1) == INVALID
+    assert call(ws=0xB008) == call(lddk=120) == call(lddq=516) == ALIGN
+
+
+def test_muon(P):
+    lib, c = P.pact.lib, P.pact.c_muon_matrix
+    good = [0x1000, 0x2000, 0x2000, 0x3000, 0x3000, 0x4000, 16, 300]
+
+    def call(n=1, ws=0x10000, size=None, lr=0.1, **at):
+        m = (c * 2)(c(*good), c(*[at.get(f[0], v) for f, v in zip(c._fields_, good)]))
+        need = lib.pact_muon_workspace_bytes(m, 2)
+        return lib.pact_muon_step(m, 2 if n == 1 else n, 0, lr, 0.9, 0.0, 1, ws, need if size is None else size, None)
+    for name in ("grad", "momentum", "momentum_out", "weight", "weight_out"):
+        assert call(**{name: None}) == INVALID
+        assert call(**{name: 0x1001}) == ALIGN
+    assert call(weight_bf16=0x4001) == ALIGN
+    assert call(rows=65, cols=65) == call(rows=0) == call(cols=2 ** 24 + 1) == SHAPE
+    assert call(n=0) == call(ws=None) == call(size=8) == call(lr=float("inf")) == INVALID
+    assert call(ws=0x10008) == ALIGN
+    assert P.pact_muon_workspace_bytes([(65, 65)]) == 0 < P.pact_muon_workspace_bytes([(64, 65)])
+
+
+def test_binding_refuses_host_tensors(P):
+    x = torch.zeros((4, 128), dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        P.pact_rope(x, torch.zeros(4, dtype=torch.int32), [0.0] * 32, 2)
+    with pytest.raises(TypeError):
+        P.pact_attention_fwd(x, x, x, torch.zeros(2, dtype=torch.int32), 2, 2)
+    with pytest.raises(TypeError):
+        P.pact_muon_step([torch.zeros(4, 8)], [torch.zeros(4, 8)], [torch.zeros(4, 8)], lr=0.1)
+    with pytest.raises(ValueError):
+        P.pact_muon_step([], [], [], lr=0.1)
