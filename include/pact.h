@@ -460,7 +460,7 @@ typedef struct {
     int64_t M;                 /* rows of q, k, v and the outputs (1 .. 2^30) */
     int heads, kv_heads;       /* heads a multiple of kv_heads */
     int head_dim;              /* 64 or 128 */
-    float scale;               /* of the scores, usually head_dim^-1/2 */
+    float scale;               /* of the scores, positive; usually head_dim^-1/2 */
     const pact_bf16 *q;        /* [M x heads*head_dim], row stride ldq */
     int64_t ldq;
     const pact_bf16 *k;        /* [M x kv_heads*head_dim], row stride ldk */

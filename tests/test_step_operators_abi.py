@@ -40,6 +40,7 @@ def attention(P, **kw):
 
 
 BAD = [(dict(q=None), INVALID), (dict(seq_start=None), INVALID), (dict(scale=float("nan")), INVALID),
+       (dict(scale=-0.125), INVALID), (dict(scale=0.0), INVALID),
        (dict(head_dim=96), SHAPE), (dict(heads=7), SHAPE), (dict(heads=0), SHAPE), (dict(kv_heads=0), SHAPE),
        (dict(M=0), SHAPE), (dict(M=2 ** 30 + 1), SHAPE), (dict(nseq=0), SHAPE), (dict(ldq=504), SHAPE),
        (dict(ldk=120), SHAPE), (dict(ldv=120), SHAPE), (dict(q=0x1008), ALIGN), (dict(k=0x2002), ALIGN),
