@@ -19,7 +19,8 @@ struct Params {
     int64_t ldq, ldk, ldv, ldo, lddo;
     pact_bf16 *o, *dq, *dk, *dv;
     int64_t lddq, lddk, lddv;
-    float *lse, *delta;         // [heads x M]
+    float *lse;                 // [heads x M]
+    float *delta, *lse2;        // [heads x M] scratch of the gradient: delta and lse log2(e)
     const int32_t *seq_start;
     int nseq, heads, kv_heads, M;
     float scale;
@@ -372,98 +373,521 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 }
 }  // namespace fwd
 
-// Rows [*b, *e) of the sequence that holds `row`; false for a row of none.
-__device__ __forceinline__ bool find_sequence(const Params &p, int row, int *b, int *e) {
-    int lo = 0, hi = p.nseq;    // last sequence with start <= row
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.seq_start[mid] <= row) lo = mid;
-        else hi = mid;
-    }
-    *b = max(p.seq_start[lo], 0);
-    *e = min(p.seq_start[lo + 1], p.M);
-    return row >= *b && row < *e;
-}
+// ------------------------------------------------------------------ gradient of q
+// The same pairs of units as the forward, sharing K and V.  A unit keeps one 128-column
+// region of tensor memory that holds S, then dP (once S is in registers), then dS as
+// BF16, the operand of dQ += dS K; so two units and their accumulators fill the 512
+// columns.  The exponentials of one unit run under the other's products:
+//   S0 S1 | dP0 dP1 | dQ0 S0(j+1) dQ1 S1(j+1) | ...
+// dq has a kernel of its own, with S and dP formed a second time for dk and dv (7 products
+// instead of 5): summing dq over key tiles from one kernel takes atomics in FP32, whose
+// order would change the result from call to call, and a pass to clear and round it.
+// This kernel also leaves delta and lse log2(e) for the other one.
+constexpr int SPLIT_THREADS = 384;   // three warpgroups; registers are moved to the first two
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+static_assert(2 * 128 * 216 + 128 * 72 <= SPLIT_THREADS * 168, "more registers than the block is launched with");
 
-template <int V>
-__device__ __forceinline__ void load_row(const pact_bf16 *p, float (&x)[V]) {
-    const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+// Sixteen columns of a lane, two BF16 values each: store `v` of 32 FP32 values.
+__device__ __forceinline__ void store_p(uint32_t taddr, const float (&v)[32]) {
+    uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-        const uint32_t u = w[i];
-        x[2 * i] = bf16lo(u);
-        x[2 * i + 1] = bf16hi(u);
-    }
+    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
+    tmem_st_32x32b_x16(taddr, w);
 }
-template <int V>
-__device__ __forceinline__ void store_row(pact_bf16 *p, const float (&x)[V]) {
-    uint32_t *w = reinterpret_cast<uint32_t *>(p);
+// N accumulator columns of a lane, times f, as BF16 to dst.
+template <int N>
+__device__ __forceinline__ void store_acc(uint32_t taddr, float f, pact_bf16 *dst, bool live) {
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-}
-template <int V>
-__device__ __forceinline__ float dot_warp(const float (&a)[V], const float (&b)[V]) {
-    float s = 0.0f;
+    for (int i = 0; i < N / 32; ++i) {
+        uint32_t a[32];
+        tmem_ld_32x32b_x32(taddr + 32 * i, a);
+        tmem_ld_wait();
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += a[i] * b[i];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
-}
-
-// dq and delta: one warp per (row, query head).
-template <int D>
-__global__ void k_attn_dq(const Params p) {
-    constexpr int V = D / 32;
-    pdl_wait();
-    const int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, h = blockIdx.y, lane = threadIdx.x & 31;
-    int b, e;
-    if (row >= p.M || !find_sequence(p, row, &b, &e)) return;
-    const int g = h / (p.heads / p.kv_heads), c = lane * V;
-    float q[V], k[V], v[V], d[V], o[V], acc[V] = {};
-    load_row(p.q + row * p.ldq + h * D + c, q);
-    load_row(p.dout + row * p.lddo + h * D + c, d);
-    load_row(p.o_in + row * p.ldo + h * D + c, o);
-    const float delta = dot_warp(d, o), lse = p.lse[(int64_t)h * p.M + row];
-    if (lane == 0) p.delta[(int64_t)h * p.M + row] = delta;
-    for (int j = b; j <= row; ++j) {
-        load_row(p.k + j * p.ldk + g * D + c, k);
-        load_row(p.v + j * p.ldv + g * D + c, v);
-        const float ds = expf(dot_warp(q, k) * p.scale - lse) * (dot_warp(d, v) - delta) * p.scale;
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += ds * k[i];
-    }
-    store_row(p.dq + row * p.lddq + h * D + c, acc);
-}
-
-// dk and dv: one warp per (row, key head), over the group's query heads and later rows.
-template <int D>
-__global__ void k_attn_dkv(const Params p) {
-    constexpr int V = D / 32;
-    pdl_wait();
-    const int row = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, g = blockIdx.y, lane = threadIdx.x & 31;
-    int b, e;
-    if (row >= p.M || !find_sequence(p, row, &b, &e)) return;
-    const int group = p.heads / p.kv_heads, c = lane * V;
-    float q[V], k[V], v[V], d[V], ak[V] = {}, av[V] = {};
-    load_row(p.k + row * p.ldk + g * D + c, k);
-    load_row(p.v + row * p.ldv + g * D + c, v);
-    for (int h = g * group; h < (g + 1) * group; ++h) {
-        for (int i = row; i < e; ++i) {
-            load_row(p.q + i * p.ldq + h * D + c, q);
-            load_row(p.dout + i * p.lddo + h * D + c, d);
-            const float w = expf(dot_warp(q, k) * p.scale - p.lse[(int64_t)h * p.M + i]);
-            const float ds = w * (dot_warp(d, v) - p.delta[(int64_t)h * p.M + i]) * p.scale;
-#pragma unroll
-            for (int t = 0; t < V; ++t) {
-                ak[t] += ds * q[t];
-                av[t] += w * d[t];
-            }
+        for (int e = 0; e < 32; e += 8) {
+            uint4 w;
+            w.x = pack_bf16x2(__uint_as_float(a[e]) * f, __uint_as_float(a[e + 1]) * f);
+            w.y = pack_bf16x2(__uint_as_float(a[e + 2]) * f, __uint_as_float(a[e + 3]) * f);
+            w.z = pack_bf16x2(__uint_as_float(a[e + 4]) * f, __uint_as_float(a[e + 5]) * f);
+            w.w = pack_bf16x2(__uint_as_float(a[e + 6]) * f, __uint_as_float(a[e + 7]) * f);
+            if (live) *reinterpret_cast<uint4 *>(dst + 32 * i + e) = w;
         }
     }
-    store_row(p.dk + row * p.lddk + g * D + c, ak);
-    store_row(p.dv + row * p.lddv + g * D + c, av);
 }
+
+namespace dq {
+template <int D>
+struct Layout {
+    static constexpr int TILE_BYTES = D / 64 * BOX_BYTES;
+    static constexpr int SMEM = 1024 + 7 * TILE_BYTES + 256;   // Q0 Q1 dO0 dO1, K twice, V
+};
+
+template <int D>
+__global__ void __launch_bounds__(SPLIT_THREADS, 1)
+k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+          const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p,
+          const Slots sl) {
+    constexpr int TB = Layout<D>::TILE_BYTES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *sk = smem + 4 * TB, *sv = smem + 6 * TB;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + 7 * TB);
+    uint64_t *q_full = bars, *tail = bars + 1, *v_full = bars + 2, *v_empty = bars + 3, *k_full = bars + 4,
+             *k_empty = bars + 6, *s_full = bars + 8, *s_read = bars + 10, *dp_full = bars + 12,
+             *ds_ready = bars + 14, *dq_full = bars + 16;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 18; ++i) mbar_init(&bars[i], (i >= 10 && i < 12) || (i >= 14 && i < 16) ? 4 : 1);
+        fence_barrier_init();
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmG);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    pdl_wait();
+    const int g = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
+    int b, len, item;
+    find_slot(p, sl, gridDim.x / p.kv_heads - 1 - blockIdx.x / p.kv_heads, lane, &b, &len, &item);
+    const int64_t units = (int64_t)((len + TILE - 1) / TILE) * group, u0 = 2 * (int64_t)item;
+    if (u0 >= units) return;   // block-uniform, before tensor memory is allocated
+    const bool two = u0 + 1 < units;
+    const int t0 = (int)(u0 / group), h0 = g * group + (int)(u0 % group);
+    const int t1 = two ? (int)((u0 + 1) / group) : t0, h1 = g * group + (int)((u0 + 1) % group);
+    const int blocks = t1 + 1;
+
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;   // regions of 128 columns, then dQ0, dQ1: D columns each
+
+    if (warp >= 8) {
+        regs_down();
+        if (warp == 8) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, (two ? 4 : 2) * TB);
+                load_tile<D>(smem, &tmQ, q_full, h0 * D, b + t0 * TILE);
+                load_tile<D>(smem + 2 * TB, &tmG, q_full, h0 * D, b + t0 * TILE);
+                if (two) {
+                    load_tile<D>(smem + TB, &tmQ, q_full, h1 * D, b + t1 * TILE);
+                    load_tile<D>(smem + 3 * TB, &tmG, q_full, h1 * D, b + t1 * TILE);
+                }
+            }
+            bool ok = true;
+            int nk = 0, nv = 0;
+            for (int j = 0; j < blocks; ++j) {
+                const int row = b + j * TILE, rows = len - j * TILE;
+                uint8_t *dst = sk + (j & 1) * TB;
+                if (!(ok = warp_all(mbar_wait(&k_empty[j & 1], ((j >> 1) & 1) ^ 1)))) break;
+                if (rows < TILE) {   // the sequence's last K tile
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(tail, TB);
+                        load_tile<D>(dst, &tmK, tail, g * D, row);
+                    }
+                    if (!(ok = warp_all(mbar_wait(tail, 0)))) break;
+                    clear_rows<D>(dst, rows, lane);
+                    if (lane == 0) mbar_arrive(&k_full[j & 1]);
+                } else if (lane == 0) {
+                    mbar_arrive_expect_tx(&k_full[j & 1], TB);
+                    load_tile<D>(dst, &tmK, &k_full[j & 1], g * D, row);
+                }
+                ++nk;
+                if (!(ok = warp_all(mbar_wait(v_empty, (j & 1) ^ 1)))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(v_full, TB);
+                    load_tile<D>(sv, &tmV, v_full, g * D, row);
+                }
+                ++nv;
+            }
+            // every copy lands before the CTA may leave
+            mbar_wait(q_full, 0);
+            if (nk > 0) mbar_wait(&k_full[(nk - 1) & 1], ((nk - 1) >> 1) & 1);
+            if (nk > 1) mbar_wait(&k_full[nk & 1], ((nk - 2) >> 1) & 1);
+            if (nv > 0) mbar_wait(v_full, (nv - 1) & 1);
+        } else if (warp == 9) {
+            const uint32_t base = smem_u32(smem), k0 = smem_u32(sk), v0 = smem_u32(sv);
+            bool ok = warp_all(mbar_wait(q_full, 0)) && warp_all(mbar_wait(&k_full[0], 0));
+            tc_fence_after();
+            if (ok) {
+                mma_cols<D>(tmem, base, k0);
+                tc_commit_w(&s_full[0]);
+                if (two) {
+                    mma_cols<D>(tmem + TILE, base + TB, k0);
+                    tc_commit_w(&s_full[1]);
+                }
+            }
+            for (int j = 0; j < blocks && ok; ++j) {
+                if (!(ok = warp_all(mbar_wait(v_full, j & 1)))) break;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u ? !two : j > t0) continue;
+                    if (!(ok = warp_all(mbar_wait(&s_read[u], j & 1)))) break;
+                    tc_fence_after();
+                    mma_cols<D>(tmem + u * TILE, base + (2 + u) * TB, v0);
+                    tc_commit_w(&dp_full[u]);
+                }
+                if (!ok) break;
+                tc_commit_w(v_empty);
+                const uint32_t kj = k0 + (j & 1) * TB, kn = k0 + ((j + 1) & 1) * TB;
+                bool next = false;
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    if (u ? !two : j > t0) continue;
+                    if (!(ok = warp_all(mbar_wait(&ds_ready[u], j & 1)))) break;
+                    tc_fence_after();
+                    mma_rows<D>(tmem + 2 * TILE + u * D, tmem + u * TILE, kj, j > 0);
+                    if (j == (u ? t1 : t0)) {
+                        tc_commit_w(&dq_full[u]);
+                        continue;
+                    }
+                    if (!next) {
+                        if (!(ok = warp_all(mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)))) break;
+                        tc_fence_after();
+                        next = true;
+                    }
+                    mma_cols<D>(tmem + u * TILE, base + u * TB, kn);
+                    tc_commit_w(&s_full[u]);
+                }
+                if (ok) tc_commit_w(&k_empty[j & 1]);
+            }
+            __syncwarp();
+        }
+    } else {
+        regs_up();
+        const int u = warp >> 2, row = threadIdx.x & 127, t = u ? t1 : t0, h = u ? h1 : h0;
+        const int last = u && !two ? -1 : t;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t X = tmem + u * TILE + lanes, Q = tmem + 2 * TILE + u * D + lanes;
+        const float c = p.scale * LOG2E;
+        const int qi = t * TILE + row;
+        const bool live = last >= 0 && qi < len;
+        const int64_t at = b + qi, stat = (int64_t)h * p.M + at;
+        float delta = 0.0f, lse2 = 0.0f;
+        if (live) {
+            const uint4 *o = reinterpret_cast<const uint4 *>(p.o_in + at * p.ldo + (int64_t)h * D);
+            const uint4 *d = reinterpret_cast<const uint4 *>(p.dout + at * p.lddo + (int64_t)h * D);
+            float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                float x[8], y[8];
+                unpack8_bf16(o[i], x);
+                unpack8_bf16(d[i], y);
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    s0 = fmaf(x[e], y[e], s0);
+                    s1 = fmaf(x[e + 1], y[e + 1], s1);
+                }
+            }
+            delta = s0 + s1;
+            lse2 = p.lse[stat] * LOG2E;
+            p.delta[stat] = delta;
+            p.lse2[stat] = lse2;
+        }
+        bool ok = true;
+        for (int j = 0; j <= last && ok; ++j) {
+            if (!(ok = warp_all(mbar_wait(&s_full[u], j & 1)))) break;
+            tc_fence_after();
+            uint32_t r[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(X + 32 * i, r[i]);
+            tmem_ld_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_read[u]);
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+                r[i >> 5][i & 31] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i >> 5][i & 31]), c, -lse2)));
+            if (!(ok = warp_all(mbar_wait(&dp_full[u], j & 1)))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t a[32];
+                float ds[32];
+                tmem_ld_32x32b_x32(X + 32 * i, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    ds[e] = __uint_as_float(r[i][e]) * (__uint_as_float(a[e]) - delta);
+                if (j == t) {   // the diagonal block: keys after the query
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * i + e > row) ds[e] = 0.0f;
+                }
+                store_p(X + 16 * i, ds);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ds_ready[u]);
+        }
+        ok = last >= 0 && ok && warp_all(mbar_wait(&dq_full[u], 0));
+        if (ok) {
+            tc_fence_after();
+            store_acc<D>(Q, p.scale, p.dq + at * p.lddq + (int64_t)h * D, live);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+}  // namespace dq
+
+// ------------------------------------------------------------- gradients of k and v
+// A CTA owns a tile of 128 keys of one key head and runs over the query tiles at and
+// after it, of every query head of the group: the group's sum stays in tensor memory.
+// Everything is transposed (rows are keys), so P^T and dS^T come out of the softmax warps
+// as the left operands, in tensor memory, of dV += P^T dO and dK += dS^T Q, and dO and Q
+// serve as both operands of their two products from one copy in shared memory.
+// 512 columns: S^T | dP^T | dV | dK; P^T and dS^T lie over S^T and dP^T.  Order of the MMAs:
+//   dV(n) S(n+1) | dK(n) dP(n+1): the exponentials of n+1 run under the second pair.
+// Two warpgroups share the columns: warps 0-3 take queries 0-63 of a tile, 4-7 the rest.
+namespace dkv {
+template <int D>
+struct Layout {
+    static constexpr int TILE_BYTES = D / 64 * BOX_BYTES;
+    static constexpr int STATS = 6 * TILE_BYTES;               // K, V, Q twice, dO twice
+    static constexpr int BARS = STATS + 2 * 2 * TILE * 4;      // lse2 and delta of two units
+    static constexpr int SMEM = 1024 + BARS + 256;
+};
+
+// tmem (+)= A . Y, A's contraction halves at columns 0-31 and 64-95 of its region.
+template <int D>
+__device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t a, uint32_t y, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16(TILE, D, false, true);
+#pragma unroll
+    for (int s = 0; s < TILE / 16; ++s)
+        mma_bf16_ts_w(tmem, a + (s >> 2) * 64 + (s & 3) * 8, desc_rows(y, s), idesc, accumulate || s > 0);
+}
+
+template <int D>
+__global__ void __launch_bounds__(SPLIT_THREADS, 1)
+k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
+           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p,
+           const Slots sl) {
+    constexpr int TB = Layout<D>::TILE_BYTES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *sq = smem + 2 * TB, *sg = smem + 4 * TB;
+    float *stats = reinterpret_cast<float *>(smem + Layout<D>::STATS);   // [unit & 1][lse2, delta][128]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Layout<D>::BARS);
+    uint64_t *kv_full = bars, *tail = bars + 1, *q_full = bars + 2, *q_empty = bars + 4, *g_full = bars + 6,
+             *g_empty = bars + 8, *s_full = bars + 10, *p_ready = bars + 11, *dp_full = bars + 12,
+             *ds_ready = bars + 13, *done = bars + 14;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 15);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 15; ++i) mbar_init(&bars[i], i == 11 || i == 13 ? 8 : i == 2 || i == 3 ? 2 : 1);
+        fence_barrier_init();
+        prefetch_tensormap(&tmQ);
+        prefetch_tensormap(&tmG);
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    pdl_wait();
+    const int g = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
+    int b, len, t;
+    find_slot(p, sl, blockIdx.x / p.kv_heads, lane, &b, &len, &t);
+    const int tiles = (len + TILE - 1) / TILE;
+    if (t >= tiles) return;   // block-uniform, before tensor memory is allocated
+    const int units = (tiles - t) * group;   // unit n: query tile t + n / group, head n % group of the group
+
+    if (warp == 9) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t S = tmem, dP = tmem + TILE, dV = tmem + 2 * TILE, dK = dV + D;
+
+    if (warp >= 8) {
+        regs_down();
+        if (warp == 8) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(kv_full, 2 * TB);
+                load_tile<D>(smem, &tmK, kv_full, g * D, b + t * TILE);
+                load_tile<D>(smem + TB, &tmV, kv_full, g * D, b + t * TILE);
+            }
+            int n = 0, tails = 0, i = t, hh = 0;
+            for (; n < units; ++n) {
+                const int s = n & 1, par = ((n >> 1) & 1) ^ 1, h = g * group + hh, row = b + i * TILE;
+                const int rows = len - i * TILE;
+                uint8_t *dq_ = sq + s * TB, *dg = sg + s * TB;
+                const bool partial = rows < TILE;   // the sequence's last query tile
+                uint64_t *qb = partial ? tail : &q_full[s], *gb = partial ? tail : &g_full[s];
+                // (the unit's two slots were last read two units ago; dO's is free first)
+                if (!warp_all(mbar_wait(&g_empty[s], par)) || !warp_all(mbar_wait(&q_empty[s], par))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(qb, partial ? 2 * TB : TB);
+                    load_tile<D>(dq_, &tmQ, qb, h * D, row);
+                    if (!partial) mbar_arrive_expect_tx(gb, TB);
+                    load_tile<D>(dg, &tmG, gb, h * D, row);
+                }
+                float *st = stats + s * 2 * TILE;
+#pragma unroll
+                for (int e = lane; e < TILE; e += 32) {
+                    const int64_t at = (int64_t)h * p.M + row + e;
+                    st[e] = e < rows ? p.lse2[at] : 0.0f;
+                    st[TILE + e] = e < rows ? p.delta[at] : 0.0f;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[s]);
+                if (partial) {
+                    if (!warp_all(mbar_wait(tail, tails & 1))) break;
+                    ++tails;
+                    clear_rows<D>(dq_, rows, lane);
+                    clear_rows<D>(dg, rows, lane);
+                    if (lane == 0) {
+                        mbar_arrive(&q_full[s]);
+                        mbar_arrive(&g_full[s]);
+                    }
+                }
+                if (++hh == group) { hh = 0; ++i; }
+            }
+            // every copy lands before the CTA may leave
+            mbar_wait(kv_full, 0);
+            for (int k = 1; k <= 2 && k <= n; ++k) {
+                mbar_wait(&q_full[(n - k) & 1], ((n - k) >> 1) & 1);
+                mbar_wait(&g_full[(n - k) & 1], ((n - k) >> 1) & 1);
+            }
+        } else if (warp == 9) {
+            const uint32_t k0 = smem_u32(smem), v0 = k0 + TB, q0 = smem_u32(sq), g0 = smem_u32(sg);
+            bool ok = warp_all(mbar_wait(kv_full, 0)) && warp_all(mbar_wait(&q_full[0], 0));
+            tc_fence_after();
+            if (ok) {
+                mma_cols<D>(S, k0, q0);
+                tc_commit_w(s_full);
+                ok = warp_all(mbar_wait(&g_full[0], 0));
+                tc_fence_after();
+            }
+            if (ok) {
+                mma_cols<D>(dP, v0, g0);
+                tc_commit_w(dp_full);
+            }
+            for (int n = 0; n < units && ok; ++n) {
+                const int s = n & 1, s1 = s ^ 1, par1 = ((n + 1) >> 1) & 1;
+                const bool more = n + 1 < units;
+                if (!(ok = warp_all(mbar_wait(p_ready, n & 1)))) break;
+                tc_fence_after();
+                mma_halves<D>(dV, S, g0 + s * TB, n > 0);
+                tc_commit_w(&g_empty[s]);
+                if (more) {
+                    if (!(ok = warp_all(mbar_wait(&q_full[s1], par1)))) break;
+                    tc_fence_after();
+                    mma_cols<D>(S, k0, q0 + s1 * TB);
+                    tc_commit_w(s_full);
+                }
+                if (!(ok = warp_all(mbar_wait(ds_ready, n & 1)))) break;
+                tc_fence_after();
+                mma_halves<D>(dK, dP, q0 + s * TB, n > 0);
+                tc_commit_w(&q_empty[s]);
+                if (more) {
+                    if (!(ok = warp_all(mbar_wait(&g_full[s1], par1)))) break;
+                    tc_fence_after();
+                    mma_cols<D>(dP, v0, g0 + s1 * TB);
+                    tc_commit_w(dp_full);
+                }
+            }
+            tc_commit_w(done);
+            __syncwarp();
+        }
+    } else {
+        regs_up();
+        const int half = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t off = ((uint32_t)(warp & 3) << 21) + half * 64;   // this warp's lanes and columns
+        const float c = p.scale * LOG2E;
+        bool ok = true;
+        int i = t, hh = 0;
+        for (int n = 0; n < units; ++n) {
+            const float *st = stats + (n & 1) * 2 * TILE + half * 64;
+            // a masked pair: the query is before the key, or behind the sequence
+            const int first = i == t ? row - half * 64 : 0, end = len - i * TILE - half * 64;
+            const bool edge = i == t || end < 64;
+            if (!(ok = warp_all(mbar_wait(&q_full[n & 1], (n >> 1) & 1)))) break;   // the statistics
+            if (!(ok = warp_all(mbar_wait(s_full, n & 1)))) break;
+            tc_fence_after();
+            uint32_t r[2][32];
+            tmem_ld_32x32b_x32(S + off, r[0]);
+            tmem_ld_32x32b_x32(S + off + 32, r[1]);
+            tmem_ld_wait();
+            float pr[2][32];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 ls = *reinterpret_cast<const float4 *>(st + 32 * k + e);
+                    pr[k][e] = ex2(fmaf(__uint_as_float(r[k][e]), c, -ls.x));
+                    pr[k][e + 1] = ex2(fmaf(__uint_as_float(r[k][e + 1]), c, -ls.y));
+                    pr[k][e + 2] = ex2(fmaf(__uint_as_float(r[k][e + 2]), c, -ls.z));
+                    pr[k][e + 3] = ex2(fmaf(__uint_as_float(r[k][e + 3]), c, -ls.w));
+                }
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * k + e < first || 32 * k + e >= end) pr[k][e] = 0.0f;
+                }
+                store_p(S + off + 16 * k, pr[k]);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_ready);
+            if (!(ok = warp_all(mbar_wait(dp_full, n & 1)))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t a[32];
+                tmem_ld_32x32b_x32(dP + off + 32 * k, a);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 dl = *reinterpret_cast<const float4 *>(st + TILE + 32 * k + e);
+                    pr[k][e] *= __uint_as_float(a[e]) - dl.x;
+                    pr[k][e + 1] *= __uint_as_float(a[e + 1]) - dl.y;
+                    pr[k][e + 2] *= __uint_as_float(a[e + 2]) - dl.z;
+                    pr[k][e + 3] *= __uint_as_float(a[e + 3]) - dl.w;
+                }
+                if (edge) {   // 0 times what is not finite
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * k + e < first || 32 * k + e >= end) pr[k][e] = 0.0f;
+                }
+                store_p(dP + off + 16 * k, pr[k]);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(ds_ready);
+            if (++hh == group) { hh = 0; ++i; }
+        }
+        ok = ok && warp_all(mbar_wait(done, 0));
+        if (ok) {
+            tc_fence_after();
+            const int kj = t * TILE + row;
+            const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+            const int64_t at = b + kj, col = (int64_t)g * D + half * (D / 2);
+            store_acc<D / 2>(dV + lanes + half * (D / 2), 1.0f, p.dv + at * p.lddv + col, kj < len);
+            store_acc<D / 2>(dK + lanes + half * (D / 2), p.scale, p.dk + at * p.lddk + col, kj < len);
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+}  // namespace dkv
 
 static pact_status check(const pact_attention_t *a, const char *what) {
     PACT_CHECK(a && a->q && a->k && a->v && a->seq_start, PACT_ERR_INVALID_ARG, "%s: NULL argument", what);
@@ -473,6 +897,7 @@ static pact_status check(const pact_attention_t *a, const char *what) {
                "%s: heads must be a multiple of kv_heads, at most 32768 (got %d, %d)", what, a->heads, a->kv_heads);
     PACT_CHECK(a->M >= 1 && a->M <= (1 << 30) && a->nseq >= 1 && a->nseq <= (1 << 20), PACT_ERR_SHAPE,
                "%s: M in [1, 2^30] and nseq in [1, 2^20] (got %lld, %d)", what, (long long)a->M, a->nseq);
+    PACT_CHECK((a->M / TILE + 1) * a->heads <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many tiles", what);
     PACT_CHECK(std::isfinite(a->scale) && a->scale > 0, PACT_ERR_INVALID_ARG, "%s: scale must be positive and finite",
                what);
     const int64_t nq = (int64_t)a->heads * a->head_dim, nk = (int64_t)a->kv_heads * a->head_dim;
@@ -512,6 +937,13 @@ static pact_status map_rows(CUtensorMap *m, const pact_bf16 *base, int64_t cols,
     return lmma::map_bf16(m, base, cols, M, ld, 64, TILE, what);
 }
 
+// The slots of pairs of units: a sequence has ceil(tiles group / 2) pairs, at most
+// len group / 256 + 127 group / 256 + 1/2.
+static Slots pair_slots(const Params &p) {
+    const int group = p.heads / p.kv_heads;
+    return {group, 2 * TILE, group / 2 + 2};
+}
+
 template <int D>
 static pact_status run_fwd(const Params &p, cudaStream_t st) {
     const char *what = "pact_attention_fwd";
@@ -522,13 +954,34 @@ static pact_status run_fwd(const Params &p, cudaStream_t st) {
     if (s == PACT_OK) s = map_rows(&k, p.k, (int64_t)p.kv_heads * D, p.M, p.ldk, what);
     if (s == PACT_OK) s = map_rows(&v, p.v, (int64_t)p.kv_heads * D, p.M, p.ldv, what);
     if (s != PACT_OK) return s;
-    // pairs of units: ceil(tiles group / 2) a sequence, at most len group / 256 + 127 group / 256 + 1/2
-    const int group = p.heads / p.kv_heads;
-    const Slots sl = {group, 2 * TILE, group / 2 + 2};
+    const Slots sl = pair_slots(p);
     const int64_t grid = sl.first(p.M, p.nseq) * p.kv_heads;
     PACT_CHECK(grid <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many tiles", what);
     return launch_dep(fwd::k_attn_fwd<D>, dim3((unsigned)grid), dim3(fwd::THREADS), fwd::Layout<D>::SMEM, st, what, q,
                       k, v, p, sl);
+}
+
+template <int D>
+static pact_status run_bwd(const Params &p, cudaStream_t st) {
+    const char *what = "pact_attention_bwd";
+    static std::atomic<uint64_t> done_q{0}, done_kv{0};
+    pact_status s = allow_smem(dq::k_attn_dq<D>, dq::Layout<D>::SMEM, done_q, what);
+    if (s == PACT_OK) s = allow_smem(dkv::k_attn_dkv<D>, dkv::Layout<D>::SMEM, done_kv, what);
+    CUtensorMap q, g, k, v;
+    const int64_t nq = (int64_t)p.heads * D, nk = (int64_t)p.kv_heads * D;
+    if (s == PACT_OK) s = map_rows(&q, p.q, nq, p.M, p.ldq, what);
+    if (s == PACT_OK) s = map_rows(&g, p.dout, nq, p.M, p.lddo, what);
+    if (s == PACT_OK) s = map_rows(&k, p.k, nk, p.M, p.ldk, what);
+    if (s == PACT_OK) s = map_rows(&v, p.v, nk, p.M, p.ldv, what);
+    if (s != PACT_OK) return s;
+    const Slots pairs = pair_slots(p), tiles = {1, TILE, 1};
+    const int64_t grid_q = pairs.first(p.M, p.nseq) * p.kv_heads, grid_kv = tiles.first(p.M, p.nseq) * p.kv_heads;
+    PACT_CHECK(grid_q <= 0x7FFFFFFF && grid_kv <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many tiles", what);
+    s = launch_dep(dq::k_attn_dq<D>, dim3((unsigned)grid_q), dim3(SPLIT_THREADS), dq::Layout<D>::SMEM, st, what, q, g,
+                   k, v, p, pairs);
+    if (s != PACT_OK) return s;
+    return launch_dep(dkv::k_attn_dkv<D>, dim3((unsigned)grid_kv), dim3(SPLIT_THREADS), dkv::Layout<D>::SMEM, st, what,
+                      q, g, k, v, p, tiles);
 }
 
 }  // namespace attn
@@ -552,7 +1005,7 @@ pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o, int64_t 
 }
 
 size_t pact_attention_bwd_workspace_bytes(int64_t M, int heads) {
-    return M < 1 || heads < 1 ? 0 : (size_t)M * heads * sizeof(float);
+    return M < 1 || heads < 1 ? 0 : 2 * (((size_t)M * heads + 3) & ~size_t(3)) * sizeof(float);
 }
 
 pact_status pact_attention_bwd(const pact_attention_t *a, const pact_attention_grad_t *g, void *workspace,
@@ -575,13 +1028,8 @@ pact_status pact_attention_bwd(const pact_attention_t *a, const pact_attention_g
     p.lse = const_cast<float *>(g->lse);
     p.delta = static_cast<float *>(workspace);
     p.dq = g->dq; p.lddq = g->lddq; p.dk = g->dk; p.lddk = g->lddk; p.dv = g->dv; p.lddv = g->lddv;
-    const bool small = a->head_dim == 64;
-    const dim3 grid_q((p.M + 7) / 8, p.heads), grid_k((p.M + 7) / 8, p.kv_heads);
-    s = launch_dep(small ? attn::k_attn_dq<64> : attn::k_attn_dq<128>, grid_q, dim3(256), 0, (cudaStream_t)stream,
-                   what, p);
-    if (s != PACT_OK) return s;
-    return launch_dep(small ? attn::k_attn_dkv<64> : attn::k_attn_dkv<128>, grid_k, dim3(256), 0,
-                      (cudaStream_t)stream, what, p);
+    p.lse2 = p.delta + (((size_t)a->M * a->heads + 3) & ~size_t(3));
+    return a->head_dim == 64 ? attn::run_bwd<64>(p, (cudaStream_t)stream) : attn::run_bwd<128>(p, (cudaStream_t)stream);
 }
 
 }  // extern "C"
