@@ -61,6 +61,9 @@ def parse():
                     help="time the NVFP4-adapted GPTQ calibration of each weight group of the layer (one JSON line "
                          "per group)")
     ap.add_argument("--calib-tokens", type=int, default=512, help="calibration tokens for --gptq")
+    ap.add_argument("--attention", action="store_true",
+                    help="run the layer's attention core too (rotation, packed causal attention, their gradients) "
+                         "instead of taking its output and gradient as given")
     ap.add_argument("--two-level", action="store_true",
                     help="cache the frozen weights in the two-level variant (a power of two per tensor)")
     return ap.parse_args()
@@ -372,7 +375,21 @@ def config_block(name, M):
 
 
 # ------------------------------------------------------------------ GPU arm
-def make_layer(name, dev, two_level=False, grad_fp32=False):
+# Head size of the layer workloads' attention core, and the base of its rotation.
+HEADS = {"llama-3.2-1b": (64, 5e5), "qwen2.5-1.5b": (128, 1e6), "llama-3.2-3b": (128, 5e5)}
+
+
+def attention_core(name, dev):
+    """The workload's attention core: batch sequences of seq tokens packed one behind the other."""
+    import torch
+    import synth
+    from nvfp4_gemm_b200.layer import AttentionCore
+    c, (D, theta) = synth.LAYERS[name], HEADS[name]
+    starts = torch.arange(c["batch"] + 1, dtype=torch.int32, device=dev) * c["seq"]
+    return AttentionCore(D, starts, [theta ** (-2 * i / D) for i in range(D // 2)])
+
+
+def make_layer(name, dev, two_level=False, grad_fp32=False, attention=False):
     """The layer (or the single projection) of workload `name` on device `dev` with its
     seeded synthetic inputs bound."""
     import torch
@@ -394,7 +411,8 @@ def make_layer(name, dev, two_level=False, grad_fp32=False):
     layer = PactLayer(shape, {k: d(v) for k, v in inputs["w"].items()},
                       {k: d(v) for k, v in inputs["lora_a"].items()},
                       {k: d(v) for k, v in inputs["lora_b"].items()}, d(inputs["gamma1"]), d(inputs["gamma2"]),
-                      two_level=two_level, grad_fp32=grad_fp32)
+                      two_level=two_level, grad_fp32=grad_fp32,
+                      attention=attention_core(name, dev) if attention else None)
     x_in = {k: d(inputs[k]) for k in layer.input_keys}
     layer.bind(*(x_in[k] for k in layer.input_keys))
     return inputs, layer, x_in
@@ -451,6 +469,9 @@ def op_table(a, layer, dev):
         if op.kind == "gemm":
             tf = op.flops / (ms / 1e3) / 1e12
             row.update({"tflops": round(tf, 1), "frac_fp4_peak": round(tf / (FP4_PER_BF16 * pk["bf16"]), 3)})
+        elif op.kind == "attention":
+            tf = op.flops / (ms / 1e3) / 1e12
+            row.update({"tflops": round(tf, 1), "frac_bf16_peak": round(tf / pk["bf16"], 3)})
         print(json.dumps(row), flush=True)
     if P.pact_get_device_status() != 0:
         raise RuntimeError(P.pact_last_error())
@@ -588,11 +609,12 @@ def main():
     world, rank = rep.world, rep.rank
 
     M = workload_tokens(a.workload)
-    inputs, layer, x_in = make_layer(a.workload, dev, a.two_level, grad_fp32=world > 1)
+    inputs, layer, x_in = make_layer(a.workload, dev, a.two_level, grad_fp32=world > 1, attention=a.attention and a.workload != "single")
     if a.ops:
         return op_table(a, layer, dev)
     ops = layer.step_ops()
     launches_per_step = sum(op.kernels for op in ops)
+    layer_has_core = getattr(layer, "attention", None) is not None
 
     # segments: each NVFP4 GEMM alone, consecutive other ops together
     segs = []
@@ -768,7 +790,9 @@ def main():
         "warmup": a.warmup, "ms_per_step": ms_per_step, "higher_is_better": True, "scaling": "weak",
         "vs_baseline": None, "dtype": "nvfp4", "data": "synthetic",
         "config": {**config_block(a.workload, M), "parallelism": f"dp{world}" if world > 1 else "single",
-                   **({"weights": "two-level layouts (a power of two per cached tensor)"} if a.two_level else {})},
+                   **({"weights": "two-level layouts (a power of two per cached tensor)"} if a.two_level else {}),
+                   **({"attention": "the attention core runs in the step (rotation, packed causal attention, "
+                                    "their gradients)"} if layer_has_core else {})},
         "frozen_proj_tflops": tflops,
         "frac_fp4_peak": tflops / fp4_peak,
         "roofline": {"bound": "tensor", "kernel": "k_nvfp4_gemm (frozen fwd + dgrad GEMMs)",

@@ -4,7 +4,8 @@ projections, forward and backward, composed from libpact calls.
 Data flow (PACT blog summary, section "方法" (method); PACT abstract):
   forward   xq1, x1, rstd1 = RMSNorm+quantize(h)            x1 BF16 feeds LoRA only
             qkv  = NVFP4 GEMM(xq1, W_qkv) + LoRA(x1)          q|k|v concatenated along N
-            [attention core: not on the NVFP4 path; a synthetic BF16 `attn` stands in]
+            attn = attention core(qkv): off the NVFP4 path; a given BF16 `attn` stands
+                   in, or, with `attention`, rotation of q, k and packed causal attention
             h2   = h + NVFP4 GEMM(q(attn), W_o) + LoRA(attn)  residual fused in the epilogue
             xq2, x2, rstd2 = RMSNorm+quantize(h2)
             gu   = NVFP4 GEMM(xq2, W_gu) + LoRA(x2)           gate|up concatenated along N
@@ -15,7 +16,9 @@ Data flow (PACT blog summary, section "方法" (method); PACT abstract):
   backward  the input gradients run the NVFP4 dgrad GEMMs on the cached transposed,
             re-quantized weight layouts; the LoRA weight gradients read the saved
             NVFP4 copies (q/k/v, gate/up: xq; down: m~ recomputed from gq, uq) or
-            attn (o).  The attention backward is replaced by a synthetic d(qkv).
+            attn (o).  d(qkv) is given, or, with `attention`, the gradient of the core.
+  update    with `trainable`, update() steps the adapters by their orthogonalised
+            momentum (pact_muon_step) from the gradients the backward left.
 
 Every op writes into buffers allocated once here, so a whole step can be captured
 into CUDA graphs.  Nothing below computes on the host or in PyTorch kernels.
@@ -23,7 +26,7 @@ into CUDA graphs.  Nothing below computes on the host or in PyTorch kernels.
 from __future__ import annotations
 
 from dataclasses import dataclass, field
-from typing import Callable, Dict, List
+from typing import Callable, Dict, List, Optional, Sequence
 
 import torch
 
@@ -69,6 +72,26 @@ class LayerShape:
         return 2.0 * 2.0 * self.M * nk
 
 
+@dataclass
+class AttentionCore:
+    """The attention between the q|k|v and o projections: heads of head_dim (H / head_dim
+    of queries, KV / head_dim of keys and values), causal over packed sequences whose
+    rows start at seq_start (int32 on the device, one more than the sequences; rows from
+    the last entry on are padding).  inv_freq: the rotation's head_dim / 2 angles per
+    position."""
+    head_dim: int
+    seq_start: torch.Tensor
+    inv_freq: Sequence[float]
+
+
+def positions(seq_start: torch.Tensor, M: int) -> torch.Tensor:
+    """Each row's place in its packed sequence, -1 for padding (int32 [M])."""
+    cu = seq_start.long()
+    rows = torch.arange(M, device=cu.device)
+    at = torch.searchsorted(cu, rows, right=True).sub_(1).clamp_(0, cu.numel() - 2)
+    return torch.where((rows >= cu[0]) & (rows < cu[-1]), rows - cu[at], -1).int()
+
+
 class PactLayer:
     """Weights are BF16 device tensors in PyTorch [out, in] layout:
     w = {q, k, v, o, gate, up, down}; lora_a = {p: [r, in]}, lora_b = {p: [out, r]};
@@ -77,13 +100,17 @@ class PactLayer:
     cached group (pact_weight_layout_cache_scaled).  grad_fp32: the LoRA weight
     gradients are written unrounded in FP32 into one flat buffer (grad_bucket, views
     in grads32), to be summed over data-parallel replicas in one collective and then
-    rounded once to BF16 by round_grads() into `grads`."""
+    rounded once to BF16 by round_grads() into `grads`.  attention: the layer runs its
+    attention core too (rotation and packed causal attention, forward and backward)
+    instead of taking attn and d_qkv; rows of padding then hold zeros there.  trainable:
+    the layer owns copies of its adapters, FP32 masters and momenta, for update()."""
 
     input_keys = ("h", "attn", "d_out", "d_qkv")
 
     def __init__(self, shape: LayerShape, w: Dict[str, torch.Tensor], lora_a: Dict[str, torch.Tensor],
                  lora_b: Dict[str, torch.Tensor], gamma1: torch.Tensor, gamma2: torch.Tensor,
-                 two_level: bool = False, grad_fp32: bool = False, fuse_silu: bool = False):
+                 two_level: bool = False, grad_fp32: bool = False, fuse_silu: bool = False,
+                 attention: Optional[AttentionCore] = None, trainable: bool = False):
         self.s = shape
         self.two_level = two_level
         self.grad_fp32 = grad_fp32
@@ -108,9 +135,10 @@ class PactLayer:
         self.sc = {k: shape.scale * 2.0 ** -g for k, g in self.gexp.items()}
         # adapters, stacked like the weights
         self.a_qkv, self.b_qkv = cat(("q", "k", "v"), lora_a), cat(("q", "k", "v"), lora_b)
-        self.a_o, self.b_o = lora_a["o"].contiguous(), lora_b["o"].contiguous()
+        own = (lambda t: t.clone(memory_format=torch.contiguous_format)) if trainable else (lambda t: t.contiguous())
+        self.a_o, self.b_o = own(lora_a["o"]), own(lora_b["o"])
         self.a_gu, self.b_gu = cat(("gate", "up"), lora_a), cat(("gate", "up"), lora_b)
-        self.a_d, self.b_d = lora_a["down"].contiguous(), lora_b["down"].contiguous()
+        self.a_d, self.b_d = own(lora_a["down"]), own(lora_b["down"])
         self.seg_qkv = [S.H, S.H + S.KV, S.H + 2 * S.KV]
         self.seg_gu = [S.I, 2 * S.I]
         self.g1, self.g2 = gamma1, gamma2
@@ -171,6 +199,71 @@ class PactLayer:
         self.l_o_b = P.lora_struct(self.u_o, self.a_o, r, [H])
         self.l_qkv_b = P.lora_struct(self.u_qkv, self.a_qkv, 3 * r, [H])
         self.inputs = None
+        self.attention = attention
+        if attention is not None:
+            self._init_attention(dev)
+        self.trainable = trainable
+        if trainable:
+            self._init_update(dev)
+
+    def _init_attention(self, dev):
+        S, core = self.s, self.attention
+        if S.H % core.head_dim or S.KV % core.head_dim:
+            raise ValueError(f"H = {S.H} and KV = {S.KV} must be multiples of head_dim = {core.head_dim}")
+        self.heads, self.kv_heads = S.H // core.head_dim, S.KV // core.head_dim
+        self.seq_start = core.seq_start.to(device=dev, dtype=torch.int32).clone()
+        self.pos = torch.empty(S.M, dtype=torch.int32, device=dev)
+        # padding rows are never written: they hold zeros, so what follows stays finite
+        self.attn = torch.zeros((S.M, S.H), dtype=torch.bfloat16, device=dev)
+        self.lse = torch.zeros((self.heads, S.M), dtype=torch.float32, device=dev)
+        self.d_qkv = torch.zeros((S.M, S.n_qkv), dtype=torch.bfloat16, device=dev)
+        self.ws_attn = self._scratch(P.pact_attention_bwd_workspace_bytes(S.M, self.heads), dev)
+        self.input_keys = ("h", "d_out")
+        self.pack(self.seq_start)
+
+    def pack(self, seq_start: torch.Tensor):
+        """Take a batch packed another way: as many row numbers as before (empty sequences
+        fill up).  The layer's buffers are updated in place, on the current stream, so a
+        captured step follows; the op lists' FLOP counts are those of the last pack()."""
+        self.seq_start.copy_(seq_start)
+        self.pos.copy_(positions(self.seq_start, self.s.M))
+        for t in (self.attn, self.lse, self.d_qkv):
+            t.zero_()
+        n = (self.seq_start[1:] - self.seq_start[:-1]).double()
+        # per product: 2 head_dim FLOPs a (query, key) pair and query head
+        self.attention_flops = 2.0 * self.s.H * float((n * (n + 1) / 2).sum())
+
+    def _init_update(self, dev):
+        self.adapters = {"a_qkv": self.a_qkv, "b_qkv": self.b_qkv, "a_o": self.a_o, "b_o": self.b_o,
+                         "a_gu": self.a_gu, "b_gu": self.b_gu, "a_d": self.a_d, "b_d": self.b_d}
+        shapes = {k: t.shape for k, t in self.adapters.items()}
+        _, self.masters = flat_views(shapes, torch.float32, dev)
+        _, self.momenta = flat_views(shapes, torch.float32, dev)
+        for k, t in self.adapters.items():
+            self.masters[k].copy_(t)
+        self.ws_update = self._scratch(P.pact_muon_workspace_bytes([t.shape for t in self._matrices(self.masters)]),
+                                       dev)
+
+    def _matrices(self, stacked: Dict[str, torch.Tensor]) -> List[torch.Tensor]:
+        """The 14 adapter matrices of tensors stacked like the adapters, as views."""
+        ends = {"a_qkv": [r * self.s.r for r in (1, 2, 3)], "b_qkv": self.seg_qkv,
+                "a_gu": [self.s.r, 2 * self.s.r], "b_gu": self.seg_gu}
+        out = []
+        for k, t in stacked.items():
+            begin = 0
+            for end in ends.get(k, [t.shape[0]]):
+                out.append(t[begin:end])
+                begin = end
+        return out
+
+    def update(self, lr: float, momentum: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True):
+        """One step of the adapters from the gradients the backward left (the FP32 ones
+        with grad_fp32): the masters, their BF16 copies the products read, the momenta."""
+        if not self.trainable:
+            raise RuntimeError("update() needs PactLayer(..., trainable=True)")
+        P.pact_muon_step(self._matrices(self.masters), self._matrices(self.grads32 if self.grad_fp32 else self.grads),
+                         self._matrices(self.momenta), lr, momentum, weight_decay, nesterov,
+                         weights_bf16=self._matrices(self.adapters), workspace=self.ws_update)
 
     @staticmethod
     def _scratch(nbytes: int, dev) -> torch.Tensor:
@@ -179,11 +272,47 @@ class PactLayer:
         return raw[off:off + nbytes]
 
     # ------------------------------------------------------------------ op lists
-    def bind(self, h: torch.Tensor, attn: torch.Tensor, d_out: torch.Tensor, d_qkv: torch.Tensor):
-        """Attach the step's inputs: layer input h [M, H], the attention-output stand-in
-        attn [M, H], the upstream gradient d_out [M, H] and the attention-backward
-        stand-in d_qkv [M, H + 2 KV].  The op lists read these tensors in place."""
-        self.inputs = (h, attn, d_out, d_qkv)
+    def bind(self, *inputs: torch.Tensor, **named: torch.Tensor):
+        """Attach the step's inputs, by name or in the order of input_keys: layer input h
+        [M, H], the attention-output stand-in attn [M, H], the upstream gradient d_out [M, H]
+        and the attention-backward stand-in d_qkv [M, H + 2 KV]; with `attention`, h and
+        d_out alone.  The op lists read these tensors in place."""
+        given = dict(zip(self.input_keys, inputs)) | named
+        if len(given) != len(inputs) + len(named) or set(given) != set(self.input_keys):
+            raise TypeError(f"bind() takes {', '.join(self.input_keys)}")
+        if self.attention is not None:
+            given |= {"attn": self.attn, "d_qkv": self.d_qkv}
+        self.inputs = tuple(given[k] for k in PactLayer.input_keys)
+
+    def _attention_fwd_ops(self) -> List[Op]:
+        if self.attention is None:
+            return []
+        S, a, M = self.s, self.attention, self.s.M
+        q, k, v = self.qkv[:, :S.H], self.qkv[:, S.H:S.H + S.KV], self.qkv[:, S.H + S.KV:]
+        qk, n = self.qkv[:, :S.H + S.KV], self.heads + self.kv_heads
+        return [
+            Op("rope", lambda: P.pact_rope(qk, self.pos, a.inv_freq, n, y=qk), bytes=4 * M * (S.H + S.KV) + 4 * M),
+            Op("attention_fwd", lambda: P.pact_attention_fwd(q, k, v, self.seq_start, self.heads, self.kv_heads,
+                                                             o=self.attn, lse=self.lse),
+               "attention", 2 * self.attention_flops, bytes=2 * M * (2 * S.H + 2 * S.KV) + 4 * M * self.heads),
+        ]
+
+    def _attention_bwd_ops(self) -> List[Op]:
+        if self.attention is None:
+            return []
+        S, a, M = self.s, self.attention, self.s.M
+        q, k, v = self.qkv[:, :S.H], self.qkv[:, S.H:S.H + S.KV], self.qkv[:, S.H + S.KV:]
+        d = self.d_qkv
+        dqk, n = d[:, :S.H + S.KV], self.heads + self.kv_heads
+        return [
+            Op("attention_bwd", lambda: P.pact_attention_bwd(
+                self.dattn, q, k, v, self.attn, self.lse, self.seq_start, self.heads, self.kv_heads, dq=d[:, :S.H],
+                dk=d[:, S.H:S.H + S.KV], dv=d[:, S.H + S.KV:], workspace=self.ws_attn),
+               "attention", 5 * self.attention_flops, kernels=2,
+               bytes=2 * M * (4 * S.H + 4 * S.KV) + 4 * M * self.heads),
+            Op("rope_bwd", lambda: P.pact_rope(dqk, self.pos, a.inv_freq, n, y=dqk, inverse=True),
+               bytes=4 * M * (S.H + S.KV) + 4 * M),
+        ]
 
     def forward_ops(self) -> List[Op]:
         S, s = self.s, self.s.scale
@@ -203,6 +332,7 @@ class PactLayer:
                kernels=nk(H, 3 * r), bytes=lora_fwd(H, 3 * r)),
             Op("gemm_fwd_qkv", lambda: P.pact_frozen_gemm_fwd(self.xq1, self.c_qkv, self.l_qkv_f, y=self.qkv),
                "gemm", gemm(S.M, S.n_qkv, S.H), bytes=gbytes(S.n_qkv, H, 3 * r)),
+            *self._attention_fwd_ops(),
             # the LoRA product streams attn and writes its NVFP4 copy aq (the GEMM's input)
             Op("lora_fwd_o+q(attn)", lambda: P.pact_lora_fwd(attn, self.a_o, self.sc["o"], self.t_o, self.ws,
                                                              xq=self.aq),
@@ -296,7 +426,8 @@ class PactLayer:
                                                      u_gexp=self.gexp["o"], grads_fp32=f32),
                kernels=LB(H, r, False), side=True,
                bytes=lora_bwd(H, 2 * M * H, H, r)),
-            # q|k|v (d_qkv stands in for the attention backward)
+            *self._attention_bwd_ops(),
+            # q|k|v (a given d_qkv stands in for the attention backward where the layer has none)
             # U streams d_qkv and writes its NVFP4 copy dqkvq (the dgrad GEMM's input)
             Op("lora_bwd_u_qkv+q(dqkv)", lambda: P.pact_lora_bwd_u(d_qkv, self.b_qkv, r, self.seg_qkv, self.sc["qkv"],
                                                                    self.u_qkv, self.ws, dyq=self.dqkvq),
@@ -325,6 +456,8 @@ class PactLayer:
         BF16 RMSNorm outputs, m and T are dead once the forward has used them."""
         _, attn, _, _ = self.inputs
         out = {"rstd1": self.rstd1, "rstd2": self.rstd2, "attn": attn}
+        if self.attention is not None:   # its gradient reads the rotated q, k and v, and lse
+            out |= {"qkv": self.qkv, "lse": self.lse}
         for name in ("xq1", "xq2", "gq", "uq"):
             t = getattr(self, name)
             out[name + ".codes"], out[name + ".scales"] = t.codes, t.scales
