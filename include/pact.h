@@ -520,18 +520,19 @@ PACT_API pact_status pact_attention_bwd(const pact_attention_t *a, const pact_at
  * are BF16, or FP32 when grad_fp32 != 0 (pact_lora_bwd's two forms).  The r x r products
  * run in FP64. */
 typedef struct {
-    const void *grad;          /* [rows x cols], contiguous, as are all below */
+    const void *grad;          /* [count x rows x cols], contiguous, as are all below */
     const float *momentum;     /* m */
     float *momentum_out;       /* m'; may be momentum itself */
     const float *weight;       /* W */
     float *weight_out;         /* W'; may be weight itself */
     pact_bf16 *weight_bf16;    /* BF16_RNE(W') or NULL */
+    int64_t count;             /* matrices of this shape, one behind the other (1 .. 2^20) */
     int64_t rows, cols;        /* the shorter at most 64, the longer at most 2^24 */
 } pact_muon_matrix_t;
-/* mats: HOST array of n matrices, read before the call returns; pointers aligned to
+/* mats: HOST array of n such entries, read before the call returns; pointers aligned to
  * their elements (16-byte aligned ones with cols a multiple of 4 are read faster).
  * Matrices must not overlap one another.  workspace: device, 16-byte aligned, >=
- * pact_muon_workspace_bytes(mats, n) (which reads rows and cols only); calls that share
+ * pact_muon_workspace_bytes(mats, n) (which reads count, rows and cols only); calls that share
  * it must not overlap on the GPU. */
 PACT_API size_t pact_muon_workspace_bytes(const pact_muon_matrix_t *mats, int n);
 PACT_API pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32, double lr,

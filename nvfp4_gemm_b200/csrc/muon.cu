@@ -48,16 +48,18 @@ struct Matrix {
     const float *w;
     float *w_out;
     pact_bf16 *w16;
-    double *parts;     // [slabs x tri x 64], then P [8 NB x 8 NB]
-    int32_t slab0;     // its first slab of the launch
+    double *parts;     // per matrix: [slabs x tri x 64], then P [8 NB x 8 NB]
+    int32_t slab0;     // first slab of the launch
+    int32_t mat0;      // first matrix of the launch
     int32_t len;       // long side
+    int32_t slabs;     // per matrix
     int16_t r;
     int16_t tall;      // stored [len x r], else [r x len]
     int16_t vec;       // 4 where every row starts 16-byte aligned and r, len allow it, else 1
 };
 
 struct Params {
-    Matrix mat[BATCH];
+    Matrix mat[BATCH];   // each of one or more matrices of one shape
     int n, grad_fp32, nesterov;
     float mu;
     double keep, lr;   // 1 - lr wd, lr
@@ -69,14 +71,28 @@ __device__ __forceinline__ void dmma(double (&c)[2], double a, double b) {
                  : "d"(a), "d"(b));
 }
 
-__device__ __forceinline__ int find_matrix(const Params &p, int slab) {
+// The entry that holds slab (BY_SLAB) or matrix number `i` of the launch, its pointers moved to the
+// matrix; *slab: the slab's number inside the matrix.
+template <int NB, bool BY_SLAB>
+__device__ __forceinline__ Matrix find_matrix(const Params &p, int i, int *slab) {
     int lo = 0, hi = p.n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.mat[mid].slab0 <= slab) lo = mid;
+        if ((BY_SLAB ? p.mat[mid].slab0 : p.mat[mid].mat0) <= i) lo = mid;
         else hi = mid;
     }
-    return lo;
+    Matrix a = p.mat[lo];
+    const int j = BY_SLAB ? (i - a.slab0) / a.slabs : i - a.mat0;
+    *slab = BY_SLAB ? i - a.slab0 - j * a.slabs : 0;
+    const int64_t off = (int64_t)j * a.r * a.len;
+    a.grad = static_cast<const uint8_t *>(a.grad) + off * (p.grad_fp32 ? 4 : 2);
+    a.m += off;
+    a.m_out += off;
+    a.w += off;
+    a.w_out += off;
+    if (a.w16) a.w16 += off;
+    a.parts += (int64_t)j * (a.slabs * tri(NB) * 64 + 64 * NB * NB);
+    return a;
 }
 
 // f(element offset, row of the short side, position in the slab) for every VEC-th element of a slab
@@ -145,8 +161,9 @@ __global__ void __launch_bounds__(THREADS) k_muon_gram(const __grid_constant__ P
     constexpr int L = slab_len(NB), LD = pitch(NB), T = tri(NB);
     extern __shared__ __align__(16) float us[];
     pdl_wait();
-    const Matrix &a = p.mat[find_matrix(p, blockIdx.x)];
-    const int slab = blockIdx.x - a.slab0, k0 = slab * L, n = min(L, a.len - k0);
+    int slab;
+    const Matrix a = find_matrix<NB, true>(p, blockIdx.x, &slab);
+    const int k0 = slab * L, n = min(L, a.len - k0);
     const int n4 = (n + 3) & ~3;
     // rows past r and positions past the end count as zero
     for (int t = threadIdx.x; t < 8 * NB * L; t += THREADS) {
@@ -215,8 +232,9 @@ __global__ void __launch_bounds__(THREADS) k_muon_poly(const __grid_constant__ P
     __shared__ double gain;
     double *S = sm, *Q = sm + SZ, *QS = sm + 2 * SZ, *P = sm + 3 * SZ, *P2 = sm + 4 * SZ;
     pdl_wait();
-    const Matrix &a = p.mat[blockIdx.x];
-    const int slabs = (a.len + slab_len(NB) - 1) / slab_len(NB);
+    int unused;
+    const Matrix a = find_matrix<NB, false>(p, blockIdx.x, &unused);
+    const int slabs = a.slabs;
     for (int t = threadIdx.x; t < T * 64; t += THREADS) {
         double s = 0.0;
 #pragma unroll 4
@@ -267,10 +285,10 @@ __global__ void __launch_bounds__(THREADS) k_muon_apply(const __grid_constant__ 
     extern __shared__ __align__(16) float us[];
     double *P = reinterpret_cast<double *>(us + 8 * NB * LD);
     pdl_wait();
-    const Matrix &a = p.mat[find_matrix(p, blockIdx.x)];
-    const int slab = blockIdx.x - a.slab0, k0 = slab * L, n = min(L, a.len - k0);
-    const int slabs = (a.len + L - 1) / L;
-    const double *src = a.parts + (int64_t)slabs * tri(NB) * 64;
+    int slab;
+    const Matrix a = find_matrix<NB, true>(p, blockIdx.x, &slab);
+    const int k0 = slab * L, n = min(L, a.len - k0);
+    const double *src = a.parts + (int64_t)a.slabs * tri(NB) * 64;
     for (int t = threadIdx.x; t < N * N; t += THREADS) P[t] = src[t];
     for (int t = threadIdx.x; t < 8 * NB * L; t += THREADS) {
         const int i = t / L, k = t - i * L;
@@ -320,7 +338,7 @@ __global__ void __launch_bounds__(THREADS) k_muon_apply(const __grid_constant__ 
 static int blocks_of(int r) { return r <= 16 ? 2 : r <= 32 ? 4 : r <= 48 ? 6 : 8; }
 
 template <int NB>
-static pact_status launch(const Params &p, int slabs, cudaStream_t st) {
+static pact_status launch(const Params &p, int matrices, int slabs, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};   // devices whose shared-memory limits are set
     const int d = current_device();
     if (d < 0 || d >= 64 || !(done.load(std::memory_order_acquire) >> d & 1)) {
@@ -336,7 +354,7 @@ static pact_status launch(const Params &p, int slabs, cudaStream_t st) {
     }
     const char *what = "pact_muon_step";
     pact_status s = launch_dep(k_muon_gram<NB>, dim3(slabs), dim3(THREADS), stage_smem(NB), st, what, p);
-    if (s == PACT_OK) s = launch_dep(k_muon_poly<NB>, dim3(p.n), dim3(THREADS), poly_smem(NB), st, what, p);
+    if (s == PACT_OK) s = launch_dep(k_muon_poly<NB>, dim3(matrices), dim3(THREADS), poly_smem(NB), st, what, p);
     if (s == PACT_OK) s = launch_dep(k_muon_apply<NB>, dim3(slabs), dim3(THREADS), apply_smem(NB), st, what, p);
     return s;
 }
@@ -346,14 +364,15 @@ static pact_status check(const pact_muon_matrix_t *mats, int n, const char *what
     for (int i = 0; i < n; ++i) {
         const pact_muon_matrix_t &m = mats[i];
         PACT_CHECK(m.grad && m.momentum && m.momentum_out && m.weight && m.weight_out, PACT_ERR_INVALID_ARG,
-                   "%s: matrix %d: NULL pointer", what, i);
+                   "%s: entry %d: NULL pointer", what, i);
+        PACT_CHECK(m.count >= 1 && m.count <= (1 << 20), PACT_ERR_SHAPE, "%s: entry %d: count in [1, 2^20]", what, i);
         PACT_CHECK(m.rows >= 1 && m.cols >= 1 && (m.rows <= 64 || m.cols <= 64) && m.rows <= (1 << 24) &&
                        m.cols <= (1 << 24),
-                   PACT_ERR_SHAPE, "%s: matrix %d: the shorter side is at most 64, the longer at most 2^24 (got %lld x %lld)",
+                   PACT_ERR_SHAPE, "%s: entry %d: the shorter side is at most 64, the longer at most 2^24 (got %lld x %lld)",
                    what, i, (long long)m.rows, (long long)m.cols);
         PACT_CHECK((((uintptr_t)m.momentum | (uintptr_t)m.momentum_out | (uintptr_t)m.weight | (uintptr_t)m.weight_out) &
                     3) == 0 && (((uintptr_t)m.grad | (uintptr_t)m.weight_bf16) & 1) == 0,
-                   PACT_ERR_ALIGN, "%s: matrix %d: pointers must be aligned to their elements", what, i);
+                   PACT_ERR_ALIGN, "%s: entry %d: pointers must be aligned to their elements", what, i);
     }
     return PACT_OK;
 }
@@ -369,14 +388,14 @@ size_t pact_muon_workspace_bytes(const pact_muon_matrix_t *mats, int n) {
     int r = 1;
     for (int i = 0; i < n; ++i) {
         const int64_t s = mats[i].rows < mats[i].cols ? mats[i].rows : mats[i].cols;
-        if (s < 1 || s > 64) return 0;
+        if (s < 1 || s > 64 || mats[i].count < 1) return 0;
         if (s > r) r = (int)s;
     }
     const int nb = blocks_of(r);
     size_t d = 0;
     for (int i = 0; i < n; ++i) {
         const int64_t len = mats[i].rows < mats[i].cols ? mats[i].cols : mats[i].rows;
-        d += (size_t)((len + slab_len(nb) - 1) / slab_len(nb)) * tri(nb) * 64 + 64 * nb * nb;
+        d += (size_t)mats[i].count * ((size_t)((len + slab_len(nb) - 1) / slab_len(nb)) * tri(nb) * 64 + 64 * nb * nb);
     }
     return d * sizeof(double);
 }
@@ -406,7 +425,7 @@ pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32,
     p.keep = 1.0 - lr * weight_decay;
     for (int first = 0; first < n; first += BATCH) {
         p.n = std::min(BATCH, n - first);
-        int slabs = 0;
+        int64_t slabs = 0, matrices = 0;
         for (int i = 0; i < p.n; ++i) {
             const pact_muon_matrix_t &m = mats[first + i];
             muon::Matrix &a = p.mat[i];
@@ -418,15 +437,18 @@ pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32,
             const bool al = aligned16(m.grad) && aligned16(m.momentum) && aligned16(m.momentum_out) &&
                             aligned16(m.weight) && aligned16(m.weight_out) && aligned16(m.weight_bf16);
             a.vec = al && m.cols % 4 == 0 ? 4 : 1;
-            a.slab0 = slabs;
+            a.slabs = (a.len + L - 1) / L;
+            a.slab0 = (int32_t)slabs;
+            a.mat0 = (int32_t)matrices;
             a.parts = ws;
-            const int ns = (a.len + L - 1) / L;
-            slabs += ns;
-            ws += (size_t)ns * tri(nb) * 64 + 64 * nb * nb;
+            slabs += a.slabs * m.count;
+            matrices += m.count;
+            PACT_CHECK(slabs <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many elements", what);
+            ws += (size_t)m.count * ((size_t)a.slabs * tri(nb) * 64 + 64 * nb * nb);
         }
         const cudaStream_t st = (cudaStream_t)stream;
-        s = nb == 2 ? muon::launch<2>(p, slabs, st) : nb == 4 ? muon::launch<4>(p, slabs, st)
-            : nb == 6 ? muon::launch<6>(p, slabs, st) : muon::launch<8>(p, slabs, st);
+        s = nb == 2 ? muon::launch<2>(p, (int)matrices, (int)slabs, st) : nb == 4 ? muon::launch<4>(p, (int)matrices, (int)slabs, st)
+            : nb == 6 ? muon::launch<6>(p, (int)matrices, (int)slabs, st) : muon::launch<8>(p, (int)matrices, (int)slabs, st);
         if (s != PACT_OK) return s;
     }
     return PACT_OK;

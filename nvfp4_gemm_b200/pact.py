@@ -72,7 +72,7 @@ class c_attention_grad(ctypes.Structure):
 class c_muon_matrix(ctypes.Structure):
     _fields_ = [("grad", ctypes.c_void_p), ("momentum", ctypes.c_void_p), ("momentum_out", ctypes.c_void_p),
                 ("weight", ctypes.c_void_p), ("weight_out", ctypes.c_void_p), ("weight_bf16", ctypes.c_void_p),
-                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+                ("count", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
 def _load() -> ctypes.CDLL:
@@ -117,7 +117,7 @@ def _load() -> ctypes.CDLL:
         "pact_lora_bwd": (S, [ctypes.POINTER(c_lora_bwd), P, ctypes.c_size_t, P]),
         "pact_silu_mul_bwd_quant": (S, [P, I64, NV, NV, I64, I64, P, I64, NV, P, P]),
         "pact_rmsnorm_bwd": (S, [P, I64, NV, P, P, I64, I64, P, P, NV, P]),
-        "pact_rope": (S, [P, I64, I64, I, I, P, ctypes.POINTER(ctypes.c_double), I, P, I64, P]),
+        "pact_rope": (S, [P, I64, I64, I, I, P, P, I, P, I64, P]),
         "pact_attention_fwd": (S, [ctypes.POINTER(c_attention), P, I64, P, P]),
         "pact_attention_bwd_workspace_bytes": (ctypes.c_size_t, [I64, I]),
         "pact_attention_bwd": (S, [ctypes.POINTER(c_attention), ctypes.POINTER(c_attention_grad), P, ctypes.c_size_t,
@@ -151,8 +151,15 @@ def _check(status: int):
         raise PactError(status, _lib.pact_last_error().decode())
 
 
+# The current stream's handle without a Stream object around it, where this PyTorch has that call
+# (a fifth of a short call's host time otherwise).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -619,21 +626,26 @@ def pact_rmsnorm_bwd(dy: torch.Tensor, yq: NVFP4Tensor, rstd: torch.Tensor, gamm
     return dx, dxq
 
 
-def _on(t: torch.Tensor, name: str, dtype, shape=None) -> torch.Tensor:
-    """t is a tensor of this type and shape on the current device (where the call launches)."""
+def _on(t: torch.Tensor, name: str, dtype, dev: int, shape=None) -> torch.Tensor:
+    """t is a tensor of this type and shape on device `dev`, the current one (where the call launches)."""
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA {str(dtype).replace('torch.', '')} tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {list(t.shape)}, expected {list(shape)}")
     return t
 
 
-def _matrix(t: torch.Tensor, name: str, shape=None) -> int:
+def _device(t: torch.Tensor) -> int:
+    """The current device (without asking for one on behalf of a host tensor, which _on refuses)."""
+    return torch.cuda.current_device() if t.is_cuda else -1
+
+
+def _matrix(t: torch.Tensor, name: str, dev: int, shape=None) -> int:
     """The row stride of a BF16 matrix (of this shape) with contiguous rows."""
-    _on(t, name, torch.bfloat16, shape)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    _on(t, name, torch.bfloat16, dev, shape)
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{name}: expected a matrix with contiguous rows")
     # a single row's stride is arbitrary in PyTorch: any legal one serves
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
@@ -653,42 +665,44 @@ def pact_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: Sequence[float
     """Rotate `heads` heads side by side in x [M x heads * head_dim] (row stride free, e.g. the q|k columns of
     a q|k|v output) by their rows' positions (int32 [M], negative: padding, not written).  inv_freq: the
     head_dim / 2 angles per position, host values.  y may be x (in place); inverse gives the gradient."""
-    ldx = _matrix(x, "x")
+    dev = _device(x)
+    ldx = _matrix(x, "x", dev)
     M, cols = x.shape
     if heads < 1 or cols % heads:
         raise ValueError(f"x: {cols} columns do not divide into {heads} heads")
-    _on(positions, "positions", torch.int32, (M,))
+    _on(positions, "positions", torch.int32, dev, (M,))
     if positions.stride(0) != 1 and M > 1:
         raise ValueError("positions: expected a contiguous vector")
-    freq = [float(f) for f in (inv_freq.tolist() if hasattr(inv_freq, "tolist") else inv_freq)]
-    if len(freq) != cols // heads // 2:
-        raise ValueError(f"inv_freq: {len(freq)} values, expected {cols // heads // 2}")
+    half = cols // heads // 2
+    if len(inv_freq) != half:
+        raise ValueError(f"inv_freq: {len(inv_freq)} values, expected {half}")
+    if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype == torch.float64 and not inv_freq.is_cuda
+            and inv_freq.is_contiguous()):
+        inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64, device="cpu").contiguous()
     if y is None:
         y = _new((M, cols), torch.bfloat16, x.device, stream)
-    ldy = _matrix(y, "y", (M, cols))
-    _check(_lib.pact_rope(x.data_ptr(), ldx, M, heads, cols // heads, positions.data_ptr(),
-                          (ctypes.c_double * len(freq))(*freq), int(bool(inverse)), y.data_ptr(), ldy,
-                          _stream(stream)))
+    ldy = _matrix(y, "y", dev, (M, cols))
+    _check(_lib.pact_rope(x.data_ptr(), ldx, M, heads, 2 * half, positions.data_ptr(), inv_freq.data_ptr(),
+                          int(bool(inverse)), y.data_ptr(), ldy, _stream(stream)))
     return y
 
 
-def _attention(q, k, v, seq_start, heads, kv_heads, scale) -> c_attention:
-    ldq, ldk, ldv = _matrix(q, "q"), _matrix(k, "k"), _matrix(v, "v")
-    M = q.shape[0]
-    if heads < 1 or kv_heads < 1 or q.shape[1] % heads:
-        raise ValueError(f"q: {q.shape[1]} columns do not divide into {heads} heads")
-    D = q.shape[1] // heads
-    for t, name in ((k, "k"), (v, "v")):
-        _on(t, name, torch.bfloat16, (M, kv_heads * D))
-    _on(seq_start, "seq_start", torch.int32)
+def _attention(q, k, v, seq_start, heads, kv_heads, scale, dev) -> c_attention:
+    ldq = _matrix(q, "q", dev)
+    M, cols = q.shape
+    if heads < 1 or kv_heads < 1 or cols % heads:
+        raise ValueError(f"q: {cols} columns do not divide into {heads} heads")
+    D = cols // heads
+    ldk, ldv = _matrix(k, "k", dev, (M, kv_heads * D)), _matrix(v, "v", dev, (M, kv_heads * D))
+    _on(seq_start, "seq_start", torch.int32, dev)
     if seq_start.dim() != 1 or seq_start.numel() < 2 or seq_start.stride(0) != 1:
         raise ValueError("seq_start: expected a contiguous vector of at least two row numbers")
     return c_attention(M, heads, kv_heads, D, D ** -0.5 if scale is None else float(scale), q.data_ptr(), ldq,
                        k.data_ptr(), ldk, v.data_ptr(), ldv, seq_start.data_ptr(), seq_start.numel() - 1)
 
 
-def _lse(t: torch.Tensor, shape) -> torch.Tensor:
-    _on(t, "lse", torch.float32, shape)
+def _lse(t: torch.Tensor, dev: int, shape) -> torch.Tensor:
+    _on(t, "lse", torch.float32, dev, shape)
     if not t.is_contiguous():
         raise ValueError("lse: expected a contiguous tensor")
     return t
@@ -700,13 +714,14 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_st
     """Causal attention over packed sequences: q [M x heads * D], k, v [M x kv_heads * D] (row strides free),
     seq_start int32 [sequences + 1] on the device.  Returns o [M x heads * D] and lse [heads x M]; rows of no
     sequence are not written.  scale defaults to D ** -0.5."""
-    a = _attention(q, k, v, seq_start, heads, kv_heads, scale)
+    dev = _device(q)
+    a = _attention(q, k, v, seq_start, heads, kv_heads, scale, dev)
     if o is None:
         o = _new(q.shape, torch.bfloat16, q.device, stream)
     if lse is None:
         lse = _new((heads, a.M), torch.float32, q.device, stream)
-    ldo = _matrix(o, "o", q.shape)
-    _check(_lib.pact_attention_fwd(ctypes.byref(a), o.data_ptr(), ldo, _lse(lse, (heads, a.M)).data_ptr(),
+    ldo = _matrix(o, "o", dev, q.shape)
+    _check(_lib.pact_attention_fwd(ctypes.byref(a), o.data_ptr(), ldo, _lse(lse, dev, (heads, a.M)).data_ptr(),
                                    _stream(stream)))
     return o, lse
 
@@ -721,12 +736,14 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                        dk: Optional[torch.Tensor] = None, dv: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None, stream=None):
     """dq, dk, dv of pact_attention_fwd from the gradient do of its output; o and lse are what it wrote."""
-    a = _attention(q, k, v, seq_start, heads, kv_heads, scale)
+    dev = _device(q)
+    a = _attention(q, k, v, seq_start, heads, kv_heads, scale, dev)
     new = lambda t: _new(t.shape, torch.bfloat16, q.device, stream)  # noqa: E731
     dq, dk, dv = dq if dq is not None else new(q), dk if dk is not None else new(k), dv if dv is not None else new(v)
-    g = c_attention_grad(o.data_ptr(), _matrix(o, "o", q.shape), _lse(lse, (heads, a.M)).data_ptr(), do.data_ptr(),
-                         _matrix(do, "do", q.shape), dq.data_ptr(), _matrix(dq, "dq", q.shape), dk.data_ptr(),
-                         _matrix(dk, "dk", k.shape), dv.data_ptr(), _matrix(dv, "dv", v.shape))
+    g = c_attention_grad(o.data_ptr(), _matrix(o, "o", dev, q.shape), _lse(lse, dev, (heads, a.M)).data_ptr(),
+                         do.data_ptr(), _matrix(do, "do", dev, q.shape), dq.data_ptr(),
+                         _matrix(dq, "dq", dev, q.shape), dk.data_ptr(), _matrix(dk, "dk", dev, k.shape),
+                         dv.data_ptr(), _matrix(dv, "dv", dev, v.shape))
     ws = workspace
     if ws is None:
         ws = _new(pact_attention_bwd_workspace_bytes(a.M, heads), torch.uint8, q.device, stream)
@@ -741,28 +758,25 @@ def _muon_matrices(weights, grads, momenta, weights_out, momenta_out, weights_bf
     cols = (weights, grads, momenta, weights_out, momenta_out)
     if n == 0 or any(len(c) != n for c in cols) or (weights_bf16 is not None and len(weights_bf16) != n):
         raise ValueError("expected one entry per weight in every list, and at least one weight")
-    gdt = grads[0].dtype
-    if gdt not in (torch.float32, torch.bfloat16):
+    gdt, f32, dev = grads[0].dtype, torch.float32, _device(weights[0])
+    if gdt not in (f32, torch.bfloat16):
         raise TypeError("grads: expected bfloat16 or float32 tensors")
-    mats = []
-    for i, w in enumerate(weights):
-        if w.dim() not in (2, 3) or w.numel() == 0:
+    mats = (c_muon_matrix * n)()
+    for i, (w, g, m, wo, mo) in enumerate(zip(*cols)):
+        shape = w.shape
+        if len(shape) not in (2, 3) or w.numel() == 0:
             raise ValueError(f"weights[{i}]: expected a matrix or a batch of matrices")
         w16 = weights_bf16[i] if weights_bf16 is not None else None
-        parts = [("grads", grads[i], gdt), ("momenta", momenta[i], torch.float32),
-                 ("momenta_out", momenta_out[i], torch.float32), ("weights", w, torch.float32),
-                 ("weights_out", weights_out[i], torch.float32), ("weights_bf16", w16, torch.bfloat16)]
-        for name, t, dt in parts:
-            if t is None:
+        for t, name, dt in ((g, "grads", gdt), (m, "momenta", f32), (mo, "momenta_out", f32), (w, "weights", f32),
+                            (wo, "weights_out", f32), (w16, "weights_bf16", torch.bfloat16)):
+            if t is None or (t is m and name == "momenta_out") or (t is w and name == "weights_out"):
                 continue
-            _on(t, f"{name}[{i}]", dt, w.shape)
+            _on(t, name, dt, dev, shape)
             if not t.is_contiguous():
                 raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
-        rows, k = w.shape[-2:]
-        at = [(t.data_ptr(), rows * k * t.element_size()) if t is not None else (0, 0) for _, t, _ in parts]
-        mats += [c_muon_matrix(*(p + j * step if p else None for p, step in at), rows, k)
-                 for j in range(w.numel() // (rows * k))]
-    return (c_muon_matrix * len(mats))(*mats), gdt == torch.float32
+        mats[i] = (g.data_ptr(), m.data_ptr(), mo.data_ptr(), w.data_ptr(), wo.data_ptr(),
+                   w16.data_ptr() if w16 is not None else None, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1])
+    return mats, gdt == f32
 
 
 def pact_muon_step(weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], momenta: Sequence[torch.Tensor],
@@ -784,9 +798,8 @@ def pact_muon_step(weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor
 
 
 def pact_muon_workspace_bytes(shapes: Sequence[Sequence[int]]) -> int:
-    """Scratch bytes of a pact_muon_step over matrices of these (rows, cols)."""
-    mats = (c_muon_matrix * len(shapes))(*(c_muon_matrix(None, None, None, None, None, None, r, c)
-                                           for r, c in shapes))
+    """Scratch bytes of a pact_muon_step over matrices of these (rows, cols) or (count, rows, cols)."""
+    mats = (c_muon_matrix * len(shapes))(*((None,) * 6 + (1,) * (3 - len(sh)) + tuple(sh) for sh in shapes))
     return int(_lib.pact_muon_workspace_bytes(mats, len(mats)))
 
 

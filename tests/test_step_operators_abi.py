@@ -76,7 +76,7 @@ def test_attention_outputs(P):
 
 def test_muon(P):
     lib, c = P.pact.lib, P.pact.c_muon_matrix
-    good = [0x1000, 0x2000, 0x2000, 0x3000, 0x3000, 0x4000, 16, 300]
+    good = [0x1000, 0x2000, 0x2000, 0x3000, 0x3000, 0x4000, 1, 16, 300]
 
     def call(n=1, ws=0x10000, size=None, lr=0.1, **at):
         m = (c * 2)(c(*good), c(*[at.get(f[0], v) for f, v in zip(c._fields_, good)]))
@@ -86,7 +86,7 @@ def test_muon(P):
         assert call(**{name: None}) == INVALID
         assert call(**{name: 0x1001}) == ALIGN
     assert call(weight_bf16=0x4001) == ALIGN
-    assert call(rows=65, cols=65) == call(rows=0) == call(cols=2 ** 24 + 1) == SHAPE
+    assert call(rows=65, cols=65) == call(rows=0) == call(cols=2 ** 24 + 1) == call(count=0) == SHAPE
     assert call(n=0) == call(ws=None) == call(size=8) == call(lr=float("inf")) == INVALID
     assert call(ws=0x10008) == ALIGN
     assert P.pact_muon_workspace_bytes([(65, 65)]) == 0 < P.pact_muon_workspace_bytes([(64, 65)])
