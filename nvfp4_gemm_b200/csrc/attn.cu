@@ -124,6 +124,11 @@ __device__ __forceinline__ void find_slot(const Params &p, const Slots &sl, int6
     *item = it < 0 || it > 0x7FFFFFFF ? 0x7FFFFFFF : (int)it;
 }
 
+constexpr int SPLIT_THREADS = 384;   // three warpgroups; registers are moved to the first two
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
+static_assert(2 * 128 * 216 + 128 * 72 <= SPLIT_THREADS * 168, "more registers than the block is launched with");
+
 // ------------------------------------------------------------------------- forward
 // A CTA computes two units that share a key head: a unit is a 128-query tile of one query
 // head, and the units of a sequence run tile-major over the group's heads, so a pair is
@@ -140,7 +145,6 @@ __device__ __forceinline__ void find_slot(const Params &p, const Slots &sl, int6
 // first block.  S(j+1) is issued behind P V(j), so a unit that sees its scores ready
 // also knows its accumulator at rest.
 namespace fwd {
-constexpr int THREADS = 320;
 constexpr int STAGES = 4;
 template <int D>
 struct Layout {
@@ -149,7 +153,7 @@ struct Layout {
 };
 
 template <int D>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(SPLIT_THREADS, 1)
 k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
            const __grid_constant__ CUtensorMap tmV, const Params p, const Slots sl) {
     constexpr int TILE_BYTES = Layout<D>::TILE_BYTES;
@@ -199,84 +203,88 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;   // S0, S1: 128 columns each, then O0, O1: D columns each
 
-    if (warp == 8) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * TILE_BYTES);
-            load_tile<D>(smem, &tmQ, q_full, h0 * D, b + t0 * TILE);
-            if (two) load_tile<D>(smem + TILE_BYTES, &tmQ, q_full, h1 * D, b + t1 * TILE);
-        }
-        uint32_t stage = 0, phase = 0;
-        bool ok = true;
-        int issued = 0;
-        for (int i = 0; i < 2 * blocks && ok; ++i) {   // K(0), V(0), K(1), ...
-            if (!(ok = warp_all(mbar_wait(&empty[stage], phase ^ 1)))) break;
-            const int row = b + (i >> 1) * TILE, rows = len - (i >> 1) * TILE;
-            uint8_t *dst = ring + stage * TILE_BYTES;
-            if ((i & 1) && rows < TILE) {   // the sequence's last V tile
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(tail, TILE_BYTES);
-                    load_tile<D>(dst, &tmV, tail, g * D, row);
+    if (warp >= 8) {
+        regs_down();
+        if (warp == 8) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * TILE_BYTES);
+                load_tile<D>(smem, &tmQ, q_full, h0 * D, b + t0 * TILE);
+                if (two) load_tile<D>(smem + TILE_BYTES, &tmQ, q_full, h1 * D, b + t1 * TILE);
+            }
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            int issued = 0;
+            for (int i = 0; i < 2 * blocks && ok; ++i) {   // K(0), V(0), K(1), ...
+                if (!(ok = warp_all(mbar_wait(&empty[stage], phase ^ 1)))) break;
+                const int row = b + (i >> 1) * TILE, rows = len - (i >> 1) * TILE;
+                uint8_t *dst = ring + stage * TILE_BYTES;
+                if ((i & 1) && rows < TILE) {   // the sequence's last V tile
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(tail, TILE_BYTES);
+                        load_tile<D>(dst, &tmV, tail, g * D, row);
+                    }
+                    if (!(ok = warp_all(mbar_wait(tail, 0)))) break;
+                    clear_rows<D>(dst, rows, lane);
+                    if (lane == 0) mbar_arrive(&full[stage]);
+                } else if (lane == 0) {
+                    mbar_arrive_expect_tx(&full[stage], TILE_BYTES);
+                    load_tile<D>(dst, i & 1 ? &tmV : &tmK, &full[stage], g * D, row);
                 }
-                if (!(ok = warp_all(mbar_wait(tail, 0)))) break;
-                clear_rows<D>(dst, rows, lane);
-                if (lane == 0) mbar_arrive(&full[stage]);
-            } else if (lane == 0) {
-                mbar_arrive_expect_tx(&full[stage], TILE_BYTES);
-                load_tile<D>(dst, i & 1 ? &tmV : &tmK, &full[stage], g * D, row);
+                ++issued;
+                if (++stage == STAGES) { stage = 0; phase ^= 1; }
             }
-            ++issued;
-            if (++stage == STAGES) { stage = 0; phase ^= 1; }
-        }
-        // every copy lands before the CTA may leave
-        mbar_wait(q_full, 0);
-        for (int s = 0; s < STAGES && s < issued; ++s) mbar_wait(&full[s], ((issued - 1 - s) / STAGES) & 1);
-    } else if (warp == 9) {
-        const uint32_t q0 = smem_u32(smem), q1 = q0 + TILE_BYTES, r0 = smem_u32(ring);
-        const uint32_t S0 = tmem, S1 = tmem + TILE, O0 = tmem + 2 * TILE, O1 = O0 + D;
-        bool ok = warp_all(mbar_wait(q_full, 0)) && warp_all(mbar_wait(&full[0], 0));
-        tc_fence_after();
-        if (ok) {
-            mma_cols<D>(S0, q0, r0);
-            tc_commit_w(&s_full[0]);
-            if (two) {
-                mma_cols<D>(S1, q1, r0);
-                tc_commit_w(&s_full[1]);
-            }
-            tc_commit_w(&empty[0]);
-        }
-        for (int j = 0; j < blocks && ok; ++j) {
-            const int vi = 2 * j + 1, ki = vi + 1, vs = vi % STAGES, ks = ki % STAGES;
-            const bool more0 = j < t0, more1 = two && j < t1;   // another block after this one
-            if (!(ok = warp_all(mbar_wait(&full[vs], (vi / STAGES) & 1)))) break;
-            if (j <= t0) {
-                if (!(ok = warp_all(mbar_wait(&p_ready[0], j & 1)))) break;
-                tc_fence_after();
-                mma_rows<D>(O0, S0, r0 + vs * TILE_BYTES, j > 0);
-                if (!more0) tc_commit_w(&o_full[0]);
-            }
-            if (more0 || more1) {
-                if (!(ok = warp_all(mbar_wait(&full[ks], (ki / STAGES) & 1)))) break;
-                tc_fence_after();
-            }
-            if (more0) {
-                mma_cols<D>(S0, q0, r0 + ks * TILE_BYTES);
+            // every copy lands before the CTA may leave
+            mbar_wait(q_full, 0);
+            for (int s = 0; s < STAGES && s < issued; ++s) mbar_wait(&full[s], ((issued - 1 - s) / STAGES) & 1);
+        } else if (warp == 9) {
+            const uint32_t q0 = smem_u32(smem), q1 = q0 + TILE_BYTES, r0 = smem_u32(ring);
+            const uint32_t S0 = tmem, S1 = tmem + TILE, O0 = tmem + 2 * TILE, O1 = O0 + D;
+            bool ok = warp_all(mbar_wait(q_full, 0)) && warp_all(mbar_wait(&full[0], 0));
+            tc_fence_after();
+            if (ok) {
+                mma_cols<D>(S0, q0, r0);
                 tc_commit_w(&s_full[0]);
+                if (two) {
+                    mma_cols<D>(S1, q1, r0);
+                    tc_commit_w(&s_full[1]);
+                }
+                tc_commit_w(&empty[0]);
             }
-            if (two) {
-                if (!(ok = warp_all(mbar_wait(&p_ready[1], j & 1)))) break;
-                tc_fence_after();
-                mma_rows<D>(O1, S1, r0 + vs * TILE_BYTES, j > 0);
-                if (!more1) tc_commit_w(&o_full[1]);
+            for (int j = 0; j < blocks && ok; ++j) {
+                const int vi = 2 * j + 1, ki = vi + 1, vs = vi % STAGES, ks = ki % STAGES;
+                const bool more0 = j < t0, more1 = two && j < t1;   // another block after this one
+                if (!(ok = warp_all(mbar_wait(&full[vs], (vi / STAGES) & 1)))) break;
+                if (j <= t0) {
+                    if (!(ok = warp_all(mbar_wait(&p_ready[0], j & 1)))) break;
+                    tc_fence_after();
+                    mma_rows<D>(O0, S0, r0 + vs * TILE_BYTES, j > 0);
+                    if (!more0) tc_commit_w(&o_full[0]);
+                }
+                if (more0 || more1) {
+                    if (!(ok = warp_all(mbar_wait(&full[ks], (ki / STAGES) & 1)))) break;
+                    tc_fence_after();
+                }
+                if (more0) {
+                    mma_cols<D>(S0, q0, r0 + ks * TILE_BYTES);
+                    tc_commit_w(&s_full[0]);
+                }
+                if (two) {
+                    if (!(ok = warp_all(mbar_wait(&p_ready[1], j & 1)))) break;
+                    tc_fence_after();
+                    mma_rows<D>(O1, S1, r0 + vs * TILE_BYTES, j > 0);
+                    if (!more1) tc_commit_w(&o_full[1]);
+                }
+                tc_commit_w(&empty[vs]);
+                if (more1) {
+                    mma_cols<D>(S1, q1, r0 + ks * TILE_BYTES);
+                    tc_commit_w(&s_full[1]);
+                }
+                if (more0 || more1) tc_commit_w(&empty[ks]);
             }
-            tc_commit_w(&empty[vs]);
-            if (more1) {
-                mma_cols<D>(S1, q1, r0 + ks * TILE_BYTES);
-                tc_commit_w(&s_full[1]);
-            }
-            if (more0 || more1) tc_commit_w(&empty[ks]);
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        regs_up();
         const int u = warp >> 2, row = threadIdx.x & 127, t = u ? t1 : t0;
         const int last = u && !two ? -1 : t;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 tensor-memory lanes
@@ -383,11 +391,6 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // instead of 5): summing dq over key tiles from one kernel takes atomics in FP32, whose
 // order would change the result from call to call, and a pass to clear and round it.
 // This kernel also leaves delta and lse log2(e) for the other one.
-constexpr int SPLIT_THREADS = 384;   // three warpgroups; registers are moved to the first two
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 216;"); }
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 72;"); }
-static_assert(2 * 128 * 216 + 128 * 72 <= SPLIT_THREADS * 168, "more registers than the block is launched with");
-
 // Sixteen columns of a lane, two BF16 values each: store `v` of 32 FP32 values.
 __device__ __forceinline__ void store_p(uint32_t taddr, const float (&v)[32]) {
     uint32_t w[16];
@@ -957,7 +960,7 @@ static pact_status run_fwd(const Params &p, cudaStream_t st) {
     const Slots sl = pair_slots(p);
     const int64_t grid = sl.first(p.M, p.nseq) * p.kv_heads;
     PACT_CHECK(grid <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many tiles", what);
-    return launch_dep(fwd::k_attn_fwd<D>, dim3((unsigned)grid), dim3(fwd::THREADS), fwd::Layout<D>::SMEM, st, what, q,
+    return launch_dep(fwd::k_attn_fwd<D>, dim3((unsigned)grid), dim3(SPLIT_THREADS), fwd::Layout<D>::SMEM, st, what, q,
                       k, v, p, sl);
 }
 
