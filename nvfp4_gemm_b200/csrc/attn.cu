@@ -37,17 +37,91 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^x of a pair by the special-function units, which take 8 cycles a warp and value ...
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
+    float a, b;
+    f2_unpack(x, a, b);
+    return f2_pack(ex2(a), ex2(b));
+}
+// ... and by the FP32 units: x = n + f with n the nearest whole number (adding 1.5 2^23
+// rounds it into the low bits), 2^f by the polynomial of degree 4 with the least relative
+// error on [-1/2, 1/2] (Remez exchange: 2.6e-6, under the BF16 rounding of a probability by
+// a factor of 700), n added to the exponent.  Below -126 it gives about 2^-126.
+__device__ __forceinline__ uint64_t ex2_fma(uint64_t x) {
+    float a, b;
+    f2_unpack(x, a, b);
+    x = f2_pack(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+    const uint64_t magic = f2_pack(12582912.0f, 12582912.0f), minus = f2_pack(-12582912.0f, -12582912.0f);
+    const uint64_t t = f2_add(x, magic), n = f2_add(t, minus);
+    const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
+    uint64_t y = f2_fma(f, f2_pack(0.00957010201f, 0.00957010201f), f2_pack(0.0559178603f, 0.0559178603f));
+    y = f2_fma(f, y, f2_pack(0.240247448f, 0.240247448f));
+    y = f2_fma(f, y, f2_pack(0.693121815f, 0.693121815f));
+    y = f2_fma(f, y, f2_pack(0.999999261f, 0.999999261f));
+    const uint32_t lo = (uint32_t)y + ((uint32_t)t << 23), hi = (uint32_t)(y >> 32) + ((uint32_t)(t >> 32) << 23);
+    return (uint64_t)hi << 32 | lo;
+}
+// Of EX2_PERIOD pairs, EX2_BY_FMA go to the FP32 units.
+constexpr int EX2_PERIOD = 8, EX2_BY_FMA = 2;
+
+// 128 columns of a lane.
+__device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[128]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        tmem_ld_32x32b_x32(taddr + 32 * i, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * i));
+    tmem_ld_wait();
+}
+// Scores of a diagonal block: keys after the query become -infinity, in place, by a loop of
+// its own (one block of many takes it, and the code of the others stays short).
+__device__ __forceinline__ void mask_diagonal(uint32_t taddr, int row) {
+#pragma unroll 1
+    for (int i = 0; i < 128; i += 32) {
+        if (!__any_sync(0xffffffffu, i + 31 > row)) continue;
+        uint32_t a[32];
+        tmem_ld_32x32b_x32(taddr + i, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+            if (i + e > row) a[e] = 0xFF800000u;
+        tmem_st_32x32b_x32(taddr + i, a);
+    }
+    tmem_st_wait();
+}
+
 // D (+)= A(tmem) . B(smem)^T, BF16 x BF16 -> FP32, K = 16: the rows of A are tensor-memory
-// lanes, eight 32-bit columns hold its 16 BF16 values.  Lane 0 of a converged warp issues.
-__device__ __forceinline__ void mma_bf16_ts_w(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                              uint32_t accumulate) {
+// lanes, eight 32-bit columns hold its 16 BF16 values.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b32 l;\n\t"
-        "mov.u32 l, %%laneid;\n\t"
-        "setp.eq.u32 q, l, 0;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
         "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// One lane of a converged warp.  The MMA warps run as that one thread: the compiler knows
+// such a branch to be uniform, and the operands of the MMAs cost few instructions.  Beside
+// busy softmax warps a 128 x 128 x 16 MMA issues every 66 cycles this way, and only every 93
+// with a lane predicate on each instruction (64 is the tensor core's rate).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // The K-major descriptor of 16 contraction columns (step s) of a [128 x D] tile, and the
@@ -65,14 +139,15 @@ template <int D>
 __device__ __forceinline__ void mma_cols(uint32_t tmem, uint32_t x, uint32_t y) {
     constexpr uint32_t idesc = idesc_bf16(TILE, TILE, false, false);
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s) mma_bf16_w(tmem, desc_cols(x, s), desc_cols(y, s), idesc, s > 0);
+    for (int s = 0; s < D / 16; ++s) mma_bf16(tmem, desc_cols(x, s), desc_cols(y, s), idesc, s > 0);
 }
-// tmem (+)= A . Y: A [128 x 128] BF16 in tensor memory, Y a [128 x D] tile.
-template <int D>
+// tmem (+)= A . Y: A [128 x 128] BF16 in tensor memory, Y a [128 x D] tile; steps [S0, S1) of 16
+// contraction rows.
+template <int D, int S0 = 0, int S1 = TILE / 16>
 __device__ __forceinline__ void mma_rows(uint32_t tmem, uint32_t a, uint32_t y, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16(TILE, D, false, true);
 #pragma unroll
-    for (int s = 0; s < TILE / 16; ++s) mma_bf16_ts_w(tmem, a + 8 * s, desc_rows(y, s), idesc, accumulate || s > 0);
+    for (int s = S0; s < S1; ++s) mma_bf16_ts(tmem, a + 8 * s, desc_rows(y, s), idesc, accumulate || s > 0);
 }
 
 // A [128 x D] tile by TMA: column `x` of the map, rows from `row`.
@@ -91,6 +166,50 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int row, int lane) {
             *reinterpret_cast<uint4 *>(tile + b * BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
+}
+
+// N accumulator columns (from `taddr`) of a warp's 32 lanes, each times its lane's f, as BF16 to rows
+// row0 + lane of dst (leading dimension ld, first column already added), rows from `rows` on left
+// out.  A lane holds a row, so the values pass through 4 KiB of shared memory (16-byte chunk
+// c of row r at c ^ (r % 8)): stores of whole 128-byte lines, four rows an instruction.
+// Stored straight from the lanes, 32 rows an instruction, a tile took 4.4 us; this way 1.
+template <int N>
+__device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t *slab, pact_bf16 *dst, int64_t ld,
+                                           int rows, int lane) {
+    constexpr int C = N < 64 ? N : 64, CH = C / 8;   // columns at a time, their 16-byte chunks
+    const uint32_t base = smem_u32(slab);
+#pragma unroll
+    for (int i = 0; i < N; i += C) {
+#pragma unroll
+        for (int k = 0; k < C; k += 32) {
+            uint32_t a[32];
+            tmem_ld_32x32b_x32(taddr + i + k, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+                uint32_t w[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    w[q] = pack_bf16x2(__uint_as_float(a[e + 2 * q]) * f, __uint_as_float(a[e + 2 * q + 1]) * f);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 base + lane * 128 + ((((k + e) >> 3) ^ (lane & 7)) << 4)),
+                             "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                             : "memory");
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int r0 = 0; r0 < 32; r0 += 32 / CH) {
+            const int r = r0 + lane / CH, c = lane % CH;
+            uint4 w;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                         : "r"(base + r * 128 + ((c ^ (r & 7)) << 4))
+                         : "memory");
+            if (r < rows) *reinterpret_cast<uint4 *>(dst + r * ld + i + 8 * c) = w;
+        }
+        __syncwarp();
+    }
 }
 
 // Sequence s gets the work slots [slot0(s), slot0(s + 1)), at least as many as it has
@@ -162,7 +281,7 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     uint8_t *ring = smem + 2 * TILE_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(ring + STAGES * TILE_BYTES);
     uint64_t *full = bars, *empty = bars + STAGES, *q_full = bars + 2 * STAGES, *tail = q_full + 1;
-    uint64_t *s_full = tail + 1, *p_ready = s_full + 2, *o_full = p_ready + 2;
+    uint64_t *s_full = tail + 1, *p_ready = s_full + 2, *o_full = p_ready + 4;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -175,7 +294,8 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         mbar_init(tail, 1);
         for (int u = 0; u < 2; ++u) {
             mbar_init(&s_full[u], 1);
-            mbar_init(&p_ready[u], 4);
+            mbar_init(&p_ready[2 * u], 4);       // keys 0-63 of a block, 64-127
+            mbar_init(&p_ready[2 * u + 1], 4);
             mbar_init(&o_full[u], 1);
         }
         fence_barrier_init();
@@ -201,7 +321,8 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;   // S0, S1: 128 columns each, then O0, O1: D columns each
+    // all 512 columns are the block's, so they start at 0: S0, S1 (128 each), then O0, O1 (D each)
+    constexpr uint32_t tmem = 0;
 
     if (warp >= 8) {
         regs_down();
@@ -236,52 +357,57 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             // every copy lands before the CTA may leave
             mbar_wait(q_full, 0);
             for (int s = 0; s < STAGES && s < issued; ++s) mbar_wait(&full[s], ((issued - 1 - s) / STAGES) & 1);
-        } else if (warp == 9) {
+        } else if (warp == 9 && elect_one()) {
             const uint32_t q0 = smem_u32(smem), q1 = q0 + TILE_BYTES, r0 = smem_u32(ring);
             const uint32_t S0 = tmem, S1 = tmem + TILE, O0 = tmem + 2 * TILE, O1 = O0 + D;
-            bool ok = warp_all(mbar_wait(q_full, 0)) && warp_all(mbar_wait(&full[0], 0));
+            bool ok = mbar_wait(q_full, 0) && mbar_wait(&full[0], 0);
             tc_fence_after();
             if (ok) {
                 mma_cols<D>(S0, q0, r0);
-                tc_commit_w(&s_full[0]);
+                tc_commit(&s_full[0]);
                 if (two) {
                     mma_cols<D>(S1, q1, r0);
-                    tc_commit_w(&s_full[1]);
+                    tc_commit(&s_full[1]);
                 }
-                tc_commit_w(&empty[0]);
+                tc_commit(&empty[0]);
             }
             for (int j = 0; j < blocks && ok; ++j) {
                 const int vi = 2 * j + 1, ki = vi + 1, vs = vi % STAGES, ks = ki % STAGES;
                 const bool more0 = j < t0, more1 = two && j < t1;   // another block after this one
-                if (!(ok = warp_all(mbar_wait(&full[vs], (vi / STAGES) & 1)))) break;
+                if (!(ok = mbar_wait(&full[vs], (vi / STAGES) & 1))) break;
                 if (j <= t0) {
-                    if (!(ok = warp_all(mbar_wait(&p_ready[0], j & 1)))) break;
+                    if (!(ok = mbar_wait(&p_ready[0], j & 1))) break;
                     tc_fence_after();
-                    mma_rows<D>(O0, S0, r0 + vs * TILE_BYTES, j > 0);
-                    if (!more0) tc_commit_w(&o_full[0]);
+                    mma_rows<D, 0, 4>(O0, S0, r0 + vs * TILE_BYTES, j > 0);
+                    if (!(ok = mbar_wait(&p_ready[1], j & 1))) break;
+                    tc_fence_after();
+                    mma_rows<D, 4, 8>(O0, S0, r0 + vs * TILE_BYTES, true);
+                    if (!more0) tc_commit(&o_full[0]);
                 }
                 if (more0 || more1) {
-                    if (!(ok = warp_all(mbar_wait(&full[ks], (ki / STAGES) & 1)))) break;
+                    if (!(ok = mbar_wait(&full[ks], (ki / STAGES) & 1))) break;
                     tc_fence_after();
                 }
                 if (more0) {
                     mma_cols<D>(S0, q0, r0 + ks * TILE_BYTES);
-                    tc_commit_w(&s_full[0]);
+                    tc_commit(&s_full[0]);
                 }
                 if (two) {
-                    if (!(ok = warp_all(mbar_wait(&p_ready[1], j & 1)))) break;
+                    if (!(ok = mbar_wait(&p_ready[2], j & 1))) break;
                     tc_fence_after();
-                    mma_rows<D>(O1, S1, r0 + vs * TILE_BYTES, j > 0);
-                    if (!more1) tc_commit_w(&o_full[1]);
+                    mma_rows<D, 0, 4>(O1, S1, r0 + vs * TILE_BYTES, j > 0);
+                    if (!(ok = mbar_wait(&p_ready[3], j & 1))) break;
+                    tc_fence_after();
+                    mma_rows<D, 4, 8>(O1, S1, r0 + vs * TILE_BYTES, true);
+                    if (!more1) tc_commit(&o_full[1]);
                 }
-                tc_commit_w(&empty[vs]);
+                tc_commit(&empty[vs]);
                 if (more1) {
                     mma_cols<D>(S1, q1, r0 + ks * TILE_BYTES);
-                    tc_commit_w(&s_full[1]);
+                    tc_commit(&s_full[1]);
                 }
-                if (more0 || more1) tc_commit_w(&empty[ks]);
+                if (more0 || more1) tc_commit(&empty[ks]);
             }
-            __syncwarp();
         }
     } else {
         regs_up();
@@ -295,18 +421,13 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         for (int j = 0; j <= last && ok; ++j) {
             if (!(ok = warp_all(mbar_wait(&s_full[u], j & 1)))) break;
             tc_fence_after();
-            uint32_t r[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(S + 32 * i, r[i]);
-            tmem_ld_wait();
-            if (j == t) {   // the diagonal block: keys after the query
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i > row) r[i >> 5][i & 31] = 0xFF800000u;
-            }
+            if (j == t) mask_diagonal(S, row);
+            uint32_t r[128];
+            tmem_ld_row(S, r);
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 128; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(r[i >> 5][i & 31]));
+            for (int e = 0; e < 128; e += 2)
+                mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
             if (j == 0) {
                 m = top;
@@ -316,65 +437,55 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     const float f = grew ? ex2(m - top) : 1.0f;
                     if (grew) m = top;
                     l *= f;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) {
-                        uint32_t a[32];
-                        tmem_ld_32x32b_x32(O + 32 * i, a);
+#pragma unroll 1
+                    for (int i = 0; i < D / 16; ++i) {
+                        uint32_t a[16];
+                        tmem_ld_32x32b_x16(O + 16 * i, a);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
-                        tmem_st_32x32b_x32(O + 32 * i, a);
+                        for (int e = 0; e < 16; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
+                        tmem_st_32x32b_x16(O + 16 * i, a);
                     }
                 }
             }
-            float sum[4] = {};
+            const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-m, -m);
+            uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[16];
+            for (int i = 0; i < 2; ++i) {   // keys 0-63, 64-127: the first product starts on the first half
+                uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float x = ex2(fmaf(__uint_as_float(r[i][2 * e]), c, -m));
-                    const float y = ex2(fmaf(__uint_as_float(r[i][2 * e + 1]), c, -m));
-                    sum[2 * (e & 1)] += x;
-                    sum[2 * (e & 1) + 1] += y;
-                    w[e] = pack_bf16x2(x, y);
+                for (int e = 0; e < 32; ++e) {
+                    const uint64_t x = f2_fma((uint64_t)r[64 * i + 2 * e + 1] << 32 | r[64 * i + 2 * e], c2, m2);
+                    const uint64_t y = e % EX2_PERIOD < EX2_BY_FMA ? ex2_fma(x) : ex2_pair(x);
+                    sum[e & 1] = f2_add(sum[e & 1], y);
+                    float y0, y1;
+                    f2_unpack(y, y0, y1);
+                    w[e] = pack_bf16x2(y0, y1);
                 }
-                tmem_st_32x32b_x16(S + 16 * i, w);
+                tmem_st_32x32b_x32(S + 32 * i, w);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[2 * u + i]);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[u]);
+            float s0, s1;
+            f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+            l += s0 + s1;
         }
         ok = last >= 0 && ok && warp_all(mbar_wait(&o_full[u], 0));
         if (ok) {
             tc_fence_after();
-            const int qi = t * TILE + row, h = u ? h1 : h0;
-            const bool live = qi < len;
-            const float inv = 1.0f / l;
-            pact_bf16 *dst = p.o + (int64_t)(b + qi) * p.ldo + (int64_t)h * D;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                uint32_t a[32];
-                tmem_ld_32x32b_x32(O + 32 * i, a);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint4 w;
-                    w.x = pack_bf16x2(__uint_as_float(a[e]) * inv, __uint_as_float(a[e + 1]) * inv);
-                    w.y = pack_bf16x2(__uint_as_float(a[e + 2]) * inv, __uint_as_float(a[e + 3]) * inv);
-                    w.z = pack_bf16x2(__uint_as_float(a[e + 4]) * inv, __uint_as_float(a[e + 5]) * inv);
-                    w.w = pack_bf16x2(__uint_as_float(a[e + 6]) * inv, __uint_as_float(a[e + 7]) * inv);
-                    if (live) *reinterpret_cast<uint4 *>(dst + 32 * i + e) = w;
-                }
-            }
-            if (live) p.lse[(int64_t)h * p.M + b + qi] = fmaf(m, LN2, logf(l));
+            const int q0 = t * TILE + (warp & 3) * 32, h = u ? h1 : h0;   // the warp's first query
+            // the unit's Q tile is no longer read: its memory passes the output on
+            store_rows<D>(O, 1.0f / l, smem + u * TILE_BYTES + (warp & 3) * 4096,
+                          p.o + (int64_t)(b + q0) * p.ldo + (int64_t)h * D, p.ldo, len - q0, lane);
+            if (q0 + lane < len) p.lse[(int64_t)h * p.M + b + q0 + lane] = fmaf(m, LN2, logf(l));
         }
         tc_fence_before();
     }
     __syncthreads();
     if (warp == 9) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -398,26 +509,6 @@ __device__ __forceinline__ void store_p(uint32_t taddr, const float (&v)[32]) {
     for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
     tmem_st_32x32b_x16(taddr, w);
 }
-// N accumulator columns of a lane, times f, as BF16 to dst.
-template <int N>
-__device__ __forceinline__ void store_acc(uint32_t taddr, float f, pact_bf16 *dst, bool live) {
-#pragma unroll
-    for (int i = 0; i < N / 32; ++i) {
-        uint32_t a[32];
-        tmem_ld_32x32b_x32(taddr + 32 * i, a);
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(a[e]) * f, __uint_as_float(a[e + 1]) * f);
-            w.y = pack_bf16x2(__uint_as_float(a[e + 2]) * f, __uint_as_float(a[e + 3]) * f);
-            w.z = pack_bf16x2(__uint_as_float(a[e + 4]) * f, __uint_as_float(a[e + 5]) * f);
-            w.w = pack_bf16x2(__uint_as_float(a[e + 6]) * f, __uint_as_float(a[e + 7]) * f);
-            if (live) *reinterpret_cast<uint4 *>(dst + 32 * i + e) = w;
-        }
-    }
-}
-
 namespace dq {
 template <int D>
 struct Layout {
@@ -467,7 +558,8 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;   // regions of 128 columns, then dQ0, dQ1: D columns each
+    // all 512 columns, from 0: two regions of 128, then dQ0, dQ1 (D each)
+    constexpr uint32_t tmem = 0;
 
     if (warp >= 8) {
         regs_down();
@@ -512,53 +604,52 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             if (nk > 0) mbar_wait(&k_full[(nk - 1) & 1], ((nk - 1) >> 1) & 1);
             if (nk > 1) mbar_wait(&k_full[nk & 1], ((nk - 2) >> 1) & 1);
             if (nv > 0) mbar_wait(v_full, (nv - 1) & 1);
-        } else if (warp == 9) {
+        } else if (warp == 9 && elect_one()) {
             const uint32_t base = smem_u32(smem), k0 = smem_u32(sk), v0 = smem_u32(sv);
-            bool ok = warp_all(mbar_wait(q_full, 0)) && warp_all(mbar_wait(&k_full[0], 0));
+            bool ok = mbar_wait(q_full, 0) && mbar_wait(&k_full[0], 0);
             tc_fence_after();
             if (ok) {
                 mma_cols<D>(tmem, base, k0);
-                tc_commit_w(&s_full[0]);
+                tc_commit(&s_full[0]);
                 if (two) {
                     mma_cols<D>(tmem + TILE, base + TB, k0);
-                    tc_commit_w(&s_full[1]);
+                    tc_commit(&s_full[1]);
                 }
             }
             for (int j = 0; j < blocks && ok; ++j) {
-                if (!(ok = warp_all(mbar_wait(v_full, j & 1)))) break;
+                if (!(ok = mbar_wait(v_full, j & 1))) break;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (u ? !two : j > t0) continue;
-                    if (!(ok = warp_all(mbar_wait(&s_read[u], j & 1)))) break;
+                    if (!(ok = mbar_wait(&s_read[u], j & 1))) break;
                     tc_fence_after();
                     mma_cols<D>(tmem + u * TILE, base + (2 + u) * TB, v0);
-                    tc_commit_w(&dp_full[u]);
+                    tc_commit(&dp_full[u]);
                 }
                 if (!ok) break;
-                tc_commit_w(v_empty);
+                tc_commit(v_empty);
                 const uint32_t kj = k0 + (j & 1) * TB, kn = k0 + ((j + 1) & 1) * TB;
                 bool next = false;
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (u ? !two : j > t0) continue;
-                    if (!(ok = warp_all(mbar_wait(&ds_ready[u], j & 1)))) break;
+                    if (!(ok = mbar_wait(&ds_ready[u], j & 1))) break;
                     tc_fence_after();
                     mma_rows<D>(tmem + 2 * TILE + u * D, tmem + u * TILE, kj, j > 0);
                     if (j == (u ? t1 : t0)) {
-                        tc_commit_w(&dq_full[u]);
+                        tc_commit(&dq_full[u]);
                         continue;
                     }
                     if (!next) {
-                        if (!(ok = warp_all(mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)))) break;
+                        if (!(ok = mbar_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1))) break;
                         tc_fence_after();
                         next = true;
                     }
                     mma_cols<D>(tmem + u * TILE, base + u * TB, kn);
-                    tc_commit_w(&s_full[u]);
+                    tc_commit(&s_full[u]);
                 }
-                if (ok) tc_commit_w(&k_empty[j & 1]);
+                if (ok) tc_commit(&k_empty[j & 1]);
             }
-            __syncwarp();
         }
     } else {
         regs_up();
@@ -567,29 +658,37 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t X = tmem + u * TILE + lanes, Q = tmem + 2 * TILE + u * D + lanes;
         const float c = p.scale * LOG2E;
-        const int qi = t * TILE + row;
-        const bool live = last >= 0 && qi < len;
-        const int64_t at = b + qi, stat = (int64_t)h * p.M + at;
+        const int q0 = t * TILE + (warp & 3) * 32;   // the warp's first query
         float delta = 0.0f, lse2 = 0.0f;
-        if (live) {
-            const uint4 *o = reinterpret_cast<const uint4 *>(p.o_in + at * p.ldo + (int64_t)h * D);
-            const uint4 *d = reinterpret_cast<const uint4 *>(p.dout + at * p.lddo + (int64_t)h * D);
-            float s0 = 0.0f, s1 = 0.0f;
+        if (last >= 0) {
+            // delta of the warp's 32 rows, D / 8 lanes a row (whole rows of o and do at a time),
+            // then from the lanes that summed a row to the lane that owns it
+            constexpr int L = D / 8, R = 32 / L;   // lanes a row, rows a load
+            const pact_bf16 *po = p.o_in + (int64_t)h * D + (lane % L) * 8, *pd = p.dout + (int64_t)h * D + (lane % L) * 8;
+            float mine = 0.0f;
+#pragma unroll 4
+            for (int i = 0; i < L; ++i) {
+                const int r = i * R + lane / L;
+                float s = 0.0f;
+                if (q0 + r < len) {
+                    const int64_t at = b + q0 + r;
+                    float x[8], y[8];
+                    unpack8_bf16(*reinterpret_cast<const uint4 *>(po + at * p.ldo), x);
+                    unpack8_bf16(*reinterpret_cast<const uint4 *>(pd + at * p.lddo), y);
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-                float x[8], y[8];
-                unpack8_bf16(o[i], x);
-                unpack8_bf16(d[i], y);
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    s0 = fmaf(x[e], y[e], s0);
-                    s1 = fmaf(x[e + 1], y[e + 1], s1);
+                    for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
                 }
+#pragma unroll
+                for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane % L == i) mine = s;       // row i R + lane / L
             }
-            delta = s0 + s1;
-            lse2 = p.lse[stat] * LOG2E;
-            p.delta[stat] = delta;
-            p.lse2[stat] = lse2;
+            delta = __shfl_sync(0xffffffffu, mine, (lane % R) * L + lane / R);
+            if (q0 + lane < len) {
+                const int64_t stat = (int64_t)h * p.M + b + q0 + lane;
+                lse2 = p.lse[stat] * LOG2E;
+                p.delta[stat] = delta;
+                p.lse2[stat] = lse2;
+            }
         }
         bool ok = true;
         for (int j = 0; j <= last && ok; ++j) {
@@ -631,12 +730,15 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         ok = last >= 0 && ok && warp_all(mbar_wait(&dq_full[u], 0));
         if (ok) {
             tc_fence_after();
-            store_acc<D>(Q, p.scale, p.dq + at * p.lddq + (int64_t)h * D, live);
+            // the unit's Q tile is no longer read: its memory passes the output on
+            store_rows<D>(Q, p.scale, smem + u * TB + (warp & 3) * 4096,
+                          p.dq + (int64_t)(b + q0) * p.lddq + (int64_t)h * D, p.lddq, len - q0, lane);
         }
         tc_fence_before();
     }
     __syncthreads();
     if (warp == 9) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -667,7 +769,7 @@ __device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t a, uint32_t y
     constexpr uint32_t idesc = idesc_bf16(TILE, D, false, true);
 #pragma unroll
     for (int s = 0; s < TILE / 16; ++s)
-        mma_bf16_ts_w(tmem, a + (s >> 2) * 64 + (s & 3) * 8, desc_rows(y, s), idesc, accumulate || s > 0);
+        mma_bf16_ts(tmem, a + (s >> 2) * 64 + (s & 3) * 8, desc_rows(y, s), idesc, accumulate || s > 0);
 }
 
 template <int D>
@@ -710,7 +812,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t tmem = 0;   // all 512 columns
     const uint32_t S = tmem, dP = tmem + TILE, dV = tmem + 2 * TILE, dK = dV + D;
 
     if (warp >= 8) {
@@ -763,46 +865,45 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 mbar_wait(&q_full[(n - k) & 1], ((n - k) >> 1) & 1);
                 mbar_wait(&g_full[(n - k) & 1], ((n - k) >> 1) & 1);
             }
-        } else if (warp == 9) {
+        } else if (warp == 9 && elect_one()) {
             const uint32_t k0 = smem_u32(smem), v0 = k0 + TB, q0 = smem_u32(sq), g0 = smem_u32(sg);
-            bool ok = warp_all(mbar_wait(kv_full, 0)) && warp_all(mbar_wait(&q_full[0], 0));
+            bool ok = mbar_wait(kv_full, 0) && mbar_wait(&q_full[0], 0);
             tc_fence_after();
             if (ok) {
                 mma_cols<D>(S, k0, q0);
-                tc_commit_w(s_full);
-                ok = warp_all(mbar_wait(&g_full[0], 0));
+                tc_commit(s_full);
+                ok = mbar_wait(&g_full[0], 0);
                 tc_fence_after();
             }
             if (ok) {
                 mma_cols<D>(dP, v0, g0);
-                tc_commit_w(dp_full);
+                tc_commit(dp_full);
             }
             for (int n = 0; n < units && ok; ++n) {
                 const int s = n & 1, s1 = s ^ 1, par1 = ((n + 1) >> 1) & 1;
                 const bool more = n + 1 < units;
-                if (!(ok = warp_all(mbar_wait(p_ready, n & 1)))) break;
+                if (!(ok = mbar_wait(p_ready, n & 1))) break;
                 tc_fence_after();
                 mma_halves<D>(dV, S, g0 + s * TB, n > 0);
-                tc_commit_w(&g_empty[s]);
+                tc_commit(&g_empty[s]);
                 if (more) {
-                    if (!(ok = warp_all(mbar_wait(&q_full[s1], par1)))) break;
+                    if (!(ok = mbar_wait(&q_full[s1], par1))) break;
                     tc_fence_after();
                     mma_cols<D>(S, k0, q0 + s1 * TB);
-                    tc_commit_w(s_full);
+                    tc_commit(s_full);
                 }
-                if (!(ok = warp_all(mbar_wait(ds_ready, n & 1)))) break;
+                if (!(ok = mbar_wait(ds_ready, n & 1))) break;
                 tc_fence_after();
                 mma_halves<D>(dK, dP, q0 + s * TB, n > 0);
-                tc_commit_w(&q_empty[s]);
+                tc_commit(&q_empty[s]);
                 if (more) {
-                    if (!(ok = warp_all(mbar_wait(&g_full[s1], par1)))) break;
+                    if (!(ok = mbar_wait(&g_full[s1], par1))) break;
                     tc_fence_after();
                     mma_cols<D>(dP, v0, g0 + s1 * TB);
-                    tc_commit_w(dp_full);
+                    tc_commit(dp_full);
                 }
             }
-            tc_commit_w(done);
-            __syncwarp();
+            tc_commit(done);
         }
     } else {
         regs_up();
@@ -876,16 +977,18 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         ok = ok && warp_all(mbar_wait(done, 0));
         if (ok) {
             tc_fence_after();
-            const int kj = t * TILE + row;
-            const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-            const int64_t at = b + kj, col = (int64_t)g * D + half * (D / 2);
-            store_acc<D / 2>(dV + lanes + half * (D / 2), 1.0f, p.dv + at * p.lddv + col, kj < len);
-            store_acc<D / 2>(dK + lanes + half * (D / 2), p.scale, p.dk + at * p.lddk + col, kj < len);
+            const int k0 = t * TILE + (warp & 3) * 32;   // the warp's first key
+            const uint32_t cols = ((uint32_t)(warp & 3) << 21) + half * (D / 2);
+            const int64_t at = b + k0, col = (int64_t)g * D + half * (D / 2);
+            uint8_t *slab = sq + warp * 4096;            // the query tiles are no longer read
+            store_rows<D / 2>(dV + cols, 1.0f, slab, p.dv + at * p.lddv + col, p.lddv, len - k0, lane);
+            store_rows<D / 2>(dK + cols, p.scale, slab, p.dk + at * p.lddk + col, p.lddk, len - k0, lane);
         }
         tc_fence_before();
     }
     __syncthreads();
     if (warp == 9) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
