@@ -73,7 +73,7 @@ __device__ __forceinline__ uint64_t ex2_fma(uint64_t x) {
     return (uint64_t)hi << 32 | lo;
 }
 // Of EX2_PERIOD pairs, EX2_BY_FMA go to the FP32 units.
-constexpr int EX2_PERIOD = 8, EX2_BY_FMA = 2;
+constexpr int EX2_PERIOD = 8, EX2_BY_FMA = 2, EX2_BY_FMA_DQ = 2, EX2_BY_FMA_DKV = 3;
 
 // 128 columns of a lane.
 __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[128]) {
@@ -502,13 +502,6 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // instead of 5): summing dq over key tiles from one kernel takes atomics in FP32, whose
 // order would change the result from call to call, and a pass to clear and round it.
 // This kernel also leaves delta and lse log2(e) for the other one.
-// Sixteen columns of a lane, two BF16 values each: store `v` of 32 FP32 values.
-__device__ __forceinline__ void store_p(uint32_t taddr, const float (&v)[32]) {
-    uint32_t w[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(v[2 * e], v[2 * e + 1]);
-    tmem_st_32x32b_x16(taddr, w);
-}
 namespace dq {
 template <int D>
 struct Layout {
@@ -666,21 +659,30 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             constexpr int L = D / 8, R = 32 / L;   // lanes a row, rows a load
             const pact_bf16 *po = p.o_in + (int64_t)h * D + (lane % L) * 8, *pd = p.dout + (int64_t)h * D + (lane % L) * 8;
             float mine = 0.0f;
-#pragma unroll 4
-            for (int i = 0; i < L; ++i) {
-                const int r = i * R + lane / L;
-                float s = 0.0f;
-                if (q0 + r < len) {
-                    const int64_t at = b + q0 + r;
-                    float x[8], y[8];
-                    unpack8_bf16(*reinterpret_cast<const uint4 *>(po + at * p.ldo), x);
-                    unpack8_bf16(*reinterpret_cast<const uint4 *>(pd + at * p.lddo), y);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s = fmaf(x[e], y[e], s);
+            for (int i0 = 0; i0 < L; i0 += 8) {   // 16 loads in flight
+                uint4 x[8], y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = (i0 + i) * R + lane / L;
+                    const int64_t at = b + q0 + r;
+                    x[i] = y[i] = make_uint4(0, 0, 0, 0);
+                    if (q0 + r < len) {
+                        x[i] = *reinterpret_cast<const uint4 *>(po + at * p.ldo);
+                        y[i] = *reinterpret_cast<const uint4 *>(pd + at * p.lddo);
+                    }
                 }
 #pragma unroll
-                for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (lane % L == i) mine = s;       // row i R + lane / L
+                for (int i = 0; i < 8; ++i) {
+                    float u8[8], v8[8], s = 0.0f;
+                    unpack8_bf16(x[i], u8);
+                    unpack8_bf16(y[i], v8);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s = fmaf(u8[e], v8[e], s);
+#pragma unroll
+                    for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                    if (lane % L == i0 + i) mine = s;   // row (i0 + i) R + lane / L
+                }
             }
             delta = __shfl_sync(0xffffffffu, mine, (lane % R) * L + lane / R);
             if (q0 + lane < len) {
@@ -690,37 +692,40 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 p.lse2[stat] = lse2;
             }
         }
+        const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-lse2, -lse2), d2 = f2_pack(-delta, -delta);
         bool ok = true;
         for (int j = 0; j <= last && ok; ++j) {
             if (!(ok = warp_all(mbar_wait(&s_full[u], j & 1)))) break;
             tc_fence_after();
-            uint32_t r[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tmem_ld_32x32b_x32(X + 32 * i, r[i]);
-            tmem_ld_wait();
+            uint32_t r[128];
+            tmem_ld_row(X, r);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_read[u]);
+            uint64_t pr[64];
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-                r[i >> 5][i & 31] = __float_as_uint(ex2(fmaf(__uint_as_float(r[i >> 5][i & 31]), c, -lse2)));
+            for (int e = 0; e < 64; ++e) {
+                const uint64_t x = f2_fma((uint64_t)r[2 * e + 1] << 32 | r[2 * e], c2, m2);
+                pr[e] = e % EX2_PERIOD < EX2_BY_FMA_DQ ? ex2_fma(x) : ex2_pair(x);
+            }
             if (!(ok = warp_all(mbar_wait(&dp_full[u], j & 1)))) break;
             tc_fence_after();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t a[32];
-                float ds[32];
+                uint32_t a[32], w[16];
                 tmem_ld_32x32b_x32(X + 32 * i, a);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    ds[e] = __uint_as_float(r[i][e]) * (__uint_as_float(a[e]) - delta);
-                if (j == t) {   // the diagonal block: keys after the query
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * i + e > row) ds[e] = 0.0f;
+                for (int e = 0; e < 16; ++e) {
+                    float x, y;
+                    f2_unpack(f2_mul(pr[16 * i + e], f2_add((uint64_t)a[2 * e + 1] << 32 | a[2 * e], d2)), x, y);
+                    if (j == t) {   // the diagonal block: keys after the query
+                        if (32 * i + 2 * e > row) x = 0.0f;
+                        if (32 * i + 2 * e + 1 > row) y = 0.0f;
+                    }
+                    w[e] = pack_bf16x2(x, y);
                 }
-                store_p(X + 16 * i, ds);
+                tmem_st_32x32b_x16(X + 16 * i, w);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -772,6 +777,23 @@ __device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t a, uint32_t y
         mma_bf16_ts(tmem, a + (s >> 2) * 64 + (s & 3) * 8, desc_rows(y, s), idesc, accumulate || s > 0);
 }
 
+// Pairs of a masked tile: columns before `first` or from `end` on become zero.
+__device__ __forceinline__ void clear_edge(uint64_t (&v)[32], int first, int end) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        float x, y;
+        f2_unpack(v[e], x, y);
+        if (2 * e < first || 2 * e >= end) x = 0.0f;
+        if (2 * e + 1 < first || 2 * e + 1 >= end) y = 0.0f;
+        v[e] = f2_pack(x, y);
+    }
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+    float x, y;
+    f2_unpack(v, x, y);
+    return pack_bf16x2(x, y);
+}
+
 template <int D>
 __global__ void __launch_bounds__(SPLIT_THREADS, 1)
 k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
@@ -781,7 +803,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sq = smem + 2 * TB, *sg = smem + 4 * TB;
-    float *stats = reinterpret_cast<float *>(smem + Layout<D>::STATS);   // [unit & 1][lse2, delta][128]
+    float *stats = reinterpret_cast<float *>(smem + Layout<D>::STATS);   // [unit & 1][-lse2, -delta][128]
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Layout<D>::BARS);
     uint64_t *kv_full = bars, *tail = bars + 1, *q_full = bars + 2, *q_empty = bars + 4, *g_full = bars + 6,
              *g_empty = bars + 8, *s_full = bars + 10, *p_ready = bars + 11, *dp_full = bars + 12,
@@ -842,8 +864,8 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 #pragma unroll
                 for (int e = lane; e < TILE; e += 32) {
                     const int64_t at = (int64_t)h * p.M + row + e;
-                    st[e] = e < rows ? p.lse2[at] : 0.0f;
-                    st[TILE + e] = e < rows ? p.delta[at] : 0.0f;
+                    st[e] = e < rows ? -p.lse2[at] : 0.0f;
+                    st[TILE + e] = e < rows ? -p.delta[at] : 0.0f;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&q_full[s]);
@@ -909,7 +931,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         regs_up();
         const int half = warp >> 2, row = threadIdx.x & 127;
         const uint32_t off = ((uint32_t)(warp & 3) << 21) + half * 64;   // this warp's lanes and columns
-        const float c = p.scale * LOG2E;
+        const uint64_t c2 = f2_pack(p.scale * LOG2E, p.scale * LOG2E);
         bool ok = true;
         int i = t, hh = 0;
         for (int n = 0; n < units; ++n) {
@@ -920,54 +942,44 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (!(ok = warp_all(mbar_wait(&q_full[n & 1], (n >> 1) & 1)))) break;   // the statistics
             if (!(ok = warp_all(mbar_wait(s_full, n & 1)))) break;
             tc_fence_after();
-            uint32_t r[2][32];
-            tmem_ld_32x32b_x32(S + off, r[0]);
-            tmem_ld_32x32b_x32(S + off + 32, r[1]);
+            uint32_t r[64];
+            tmem_ld_32x32b_x32(S + off, *reinterpret_cast<uint32_t(*)[32]>(r));
+            tmem_ld_32x32b_x32(S + off + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
             tmem_ld_wait();
-            float pr[2][32];
+            uint64_t pr[32];
+            uint32_t w[32];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
+            for (int e = 0; e < 32; e += 2) {
+                const ulonglong2 ls = *reinterpret_cast<const ulonglong2 *>(st + 2 * e);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 ls = *reinterpret_cast<const float4 *>(st + 32 * k + e);
-                    pr[k][e] = ex2(fmaf(__uint_as_float(r[k][e]), c, -ls.x));
-                    pr[k][e + 1] = ex2(fmaf(__uint_as_float(r[k][e + 1]), c, -ls.y));
-                    pr[k][e + 2] = ex2(fmaf(__uint_as_float(r[k][e + 2]), c, -ls.z));
-                    pr[k][e + 3] = ex2(fmaf(__uint_as_float(r[k][e + 3]), c, -ls.w));
+                for (int k = e; k < e + 2; ++k) {
+                    const uint64_t x = f2_fma((uint64_t)r[2 * k + 1] << 32 | r[2 * k], c2, k == e ? ls.x : ls.y);
+                    pr[k] = k % EX2_PERIOD < EX2_BY_FMA_DKV ? ex2_fma(x) : ex2_pair(x);
                 }
-                if (edge) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * k + e < first || 32 * k + e >= end) pr[k][e] = 0.0f;
-                }
-                store_p(S + off + 16 * k, pr[k]);
             }
+            if (edge) clear_edge(pr, first, end);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = pack_pair(pr[e]);
+            tmem_st_32x32b_x32(S + off, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_ready);
             if (!(ok = warp_all(mbar_wait(dp_full, n & 1)))) break;
             tc_fence_after();
+            tmem_ld_32x32b_x32(dP + off, *reinterpret_cast<uint32_t(*)[32]>(r));
+            tmem_ld_32x32b_x32(dP + off + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+            tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t a[32];
-                tmem_ld_32x32b_x32(dP + off + 32 * k, a);
-                tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 dl = *reinterpret_cast<const float4 *>(st + TILE + 32 * k + e);
-                    pr[k][e] *= __uint_as_float(a[e]) - dl.x;
-                    pr[k][e + 1] *= __uint_as_float(a[e + 1]) - dl.y;
-                    pr[k][e + 2] *= __uint_as_float(a[e + 2]) - dl.z;
-                    pr[k][e + 3] *= __uint_as_float(a[e + 3]) - dl.w;
-                }
-                if (edge) {   // 0 times what is not finite
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * k + e < first || 32 * k + e >= end) pr[k][e] = 0.0f;
-                }
-                store_p(dP + off + 16 * k, pr[k]);
+            for (int e = 0; e < 32; e += 2) {
+                const ulonglong2 dl = *reinterpret_cast<const ulonglong2 *>(st + TILE + 2 * e);
+                pr[e] = f2_mul(pr[e], f2_add((uint64_t)r[2 * e + 1] << 32 | r[2 * e], dl.x));
+                pr[e + 1] = f2_mul(pr[e + 1], f2_add((uint64_t)r[2 * e + 3] << 32 | r[2 * e + 2], dl.y));
             }
+            if (edge) clear_edge(pr, first, end);   // 0 times what is not finite
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = pack_pair(pr[e]);
+            tmem_st_32x32b_x32(dP + off, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
