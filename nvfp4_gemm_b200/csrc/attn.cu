@@ -502,6 +502,29 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // instead of 5): summing dq over key tiles from one kernel takes atomics in FP32, whose
 // order would change the result from call to call, and a pass to clear and round it.
 // This kernel also leaves delta and lse log2(e) for the other one.
+// The gradient kernels' softmax needs no exchange between the columns of a row (lse is known), so
+// four warpgroups do it: four warps a scheduler hide one another's latencies, where two left
+// the schedulers idle two cycles in three.
+constexpr int GRAD_WARPS = 16, GRAD_THREADS = 32 * GRAD_WARPS + 128;
+__device__ __forceinline__ void grad_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 104;"); }
+__device__ __forceinline__ void grad_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
+static_assert(512 * 104 + 128 * 64 <= GRAD_THREADS * 96, "more registers than the block is launched with");
+
+// tmem (+)= A . Y: the four 32-row quarters of A's contraction lie 32 columns apart, each over the
+// first half of the 32 FP32 columns it was computed from.
+template <int D>
+__device__ __forceinline__ void mma_quarters(uint32_t tmem, uint32_t a, uint32_t y, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16(TILE, D, false, true);
+#pragma unroll
+    for (int s = 0; s < TILE / 16; ++s)
+        mma_bf16_ts(tmem, a + (s >> 1) * 32 + (s & 1) * 8, desc_rows(y, s), idesc, accumulate || s > 0);
+}
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+    float x, y;
+    f2_unpack(v, x, y);
+    return pack_bf16x2(x, y);
+}
+
 namespace dq {
 template <int D>
 struct Layout {
@@ -716,15 +739,18 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 tmem_ld_32x32b_x32(X + 32 * i, a);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float x, y;
-                    f2_unpack(f2_mul(pr[16 * i + e], f2_add((uint64_t)a[2 * e + 1] << 32 | a[2 * e], d2)), x, y);
-                    if (j == t) {   // the diagonal block: keys after the query
-                        if (32 * i + 2 * e > row) x = 0.0f;
-                        if (32 * i + 2 * e + 1 > row) y = 0.0f;
+                for (int e = 0; e < 16; ++e)
+                    pr[16 * i + e] = f2_mul(pr[16 * i + e], f2_add((uint64_t)a[2 * e + 1] << 32 | a[2 * e], d2));
+                if (j == t) {   // the diagonal block: keys after the query
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x, y;
+                        f2_unpack(pr[16 * i + e], x, y);
+                        pr[16 * i + e] = f2_pack(32 * i + 2 * e > row ? 0.0f : x, 32 * i + 2 * e + 1 > row ? 0.0f : y);
                     }
-                    w[e] = pack_bf16x2(x, y);
                 }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = pack_pair(pr[16 * i + e]);
                 tmem_st_32x32b_x16(X + 16 * i, w);
             }
             tmem_st_wait();
@@ -758,7 +784,7 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 // serve as both operands of their two products from one copy in shared memory.
 // 512 columns: S^T | dP^T | dV | dK; P^T and dS^T lie over S^T and dP^T.  Order of the MMAs:
 //   dV(n) S(n+1) | dK(n) dP(n+1): the exponentials of n+1 run under the second pair.
-// Two warpgroups share the columns: warps 0-3 take queries 0-63 of a tile, 4-7 the rest.
+// Four warpgroups share the columns: warps 4 w .. 4 w + 3 take queries 32 w .. 32 w + 31 of a tile.
 namespace dkv {
 template <int D>
 struct Layout {
@@ -768,19 +794,10 @@ struct Layout {
     static constexpr int SMEM = 1024 + BARS + 256;
 };
 
-// tmem (+)= A . Y, A's contraction halves at columns 0-31 and 64-95 of its region.
-template <int D>
-__device__ __forceinline__ void mma_halves(uint32_t tmem, uint32_t a, uint32_t y, bool accumulate) {
-    constexpr uint32_t idesc = idesc_bf16(TILE, D, false, true);
-#pragma unroll
-    for (int s = 0; s < TILE / 16; ++s)
-        mma_bf16_ts(tmem, a + (s >> 2) * 64 + (s & 3) * 8, desc_rows(y, s), idesc, accumulate || s > 0);
-}
-
 // Pairs of a masked tile: columns before `first` or from `end` on become zero.
-__device__ __forceinline__ void clear_edge(uint64_t (&v)[32], int first, int end) {
+__device__ __forceinline__ void clear_edge(uint64_t (&v)[16], int first, int end) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
+    for (int e = 0; e < 16; ++e) {
         float x, y;
         f2_unpack(v[e], x, y);
         if (2 * e < first || 2 * e >= end) x = 0.0f;
@@ -788,14 +805,9 @@ __device__ __forceinline__ void clear_edge(uint64_t (&v)[32], int first, int end
         v[e] = f2_pack(x, y);
     }
 }
-__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
-    float x, y;
-    f2_unpack(v, x, y);
-    return pack_bf16x2(x, y);
-}
 
 template <int D>
-__global__ void __launch_bounds__(SPLIT_THREADS, 1)
+__global__ void __launch_bounds__(GRAD_THREADS, 1)
 k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
            const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p,
            const Slots sl) {
@@ -812,7 +824,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 15; ++i) mbar_init(&bars[i], i == 11 || i == 13 ? 8 : i == 2 || i == 3 ? 2 : 1);
+        for (int i = 0; i < 15; ++i) mbar_init(&bars[i], i == 11 || i == 13 ? GRAD_WARPS : i == 2 || i == 3 ? 2 : 1);
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmG);
@@ -827,7 +839,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     if (t >= tiles) return;   // block-uniform, before tensor memory is allocated
     const int units = (tiles - t) * group;   // unit n: query tile t + n / group, head n % group of the group
 
-    if (warp == 9) {
+    if (warp == GRAD_WARPS + 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -837,9 +849,9 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     constexpr uint32_t tmem = 0;   // all 512 columns
     const uint32_t S = tmem, dP = tmem + TILE, dV = tmem + 2 * TILE, dK = dV + D;
 
-    if (warp >= 8) {
-        regs_down();
-        if (warp == 8) {
+    if (warp >= GRAD_WARPS) {
+        grad_regs_down();
+        if (warp == GRAD_WARPS) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(kv_full, 2 * TB);
                 load_tile<D>(smem, &tmK, kv_full, g * D, b + t * TILE);
@@ -887,7 +899,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 mbar_wait(&q_full[(n - k) & 1], ((n - k) >> 1) & 1);
                 mbar_wait(&g_full[(n - k) & 1], ((n - k) >> 1) & 1);
             }
-        } else if (warp == 9 && elect_one()) {
+        } else if (warp == GRAD_WARPS + 1 && elect_one()) {
             const uint32_t k0 = smem_u32(smem), v0 = k0 + TB, q0 = smem_u32(sq), g0 = smem_u32(sg);
             bool ok = mbar_wait(kv_full, 0) && mbar_wait(&q_full[0], 0);
             tc_fence_after();
@@ -906,7 +918,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 const bool more = n + 1 < units;
                 if (!(ok = mbar_wait(p_ready, n & 1))) break;
                 tc_fence_after();
-                mma_halves<D>(dV, S, g0 + s * TB, n > 0);
+                mma_quarters<D>(dV, S, g0 + s * TB, n > 0);
                 tc_commit(&g_empty[s]);
                 if (more) {
                     if (!(ok = mbar_wait(&q_full[s1], par1))) break;
@@ -916,7 +928,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 }
                 if (!(ok = mbar_wait(ds_ready, n & 1))) break;
                 tc_fence_after();
-                mma_halves<D>(dK, dP, q0 + s * TB, n > 0);
+                mma_quarters<D>(dK, dP, q0 + s * TB, n > 0);
                 tc_commit(&q_empty[s]);
                 if (more) {
                     if (!(ok = mbar_wait(&g_full[s1], par1))) break;
@@ -928,28 +940,26 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             tc_commit(done);
         }
     } else {
-        regs_up();
-        const int half = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t off = ((uint32_t)(warp & 3) << 21) + half * 64;   // this warp's lanes and columns
+        grad_regs_up();
+        const int quarter = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t off = ((uint32_t)(warp & 3) << 21) + quarter * 32;   // this warp's lanes and columns
         const uint64_t c2 = f2_pack(p.scale * LOG2E, p.scale * LOG2E);
         bool ok = true;
         int i = t, hh = 0;
         for (int n = 0; n < units; ++n) {
-            const float *st = stats + (n & 1) * 2 * TILE + half * 64;
+            const float *st = stats + (n & 1) * 2 * TILE + quarter * 32;
             // a masked pair: the query is before the key, or behind the sequence
-            const int first = i == t ? row - half * 64 : 0, end = len - i * TILE - half * 64;
-            const bool edge = i == t || end < 64;
+            const int first = i == t ? row - quarter * 32 : 0, end = len - i * TILE - quarter * 32;
+            const bool edge = i == t || end < 32;
             if (!(ok = warp_all(mbar_wait(&q_full[n & 1], (n >> 1) & 1)))) break;   // the statistics
             if (!(ok = warp_all(mbar_wait(s_full, n & 1)))) break;
             tc_fence_after();
-            uint32_t r[64];
-            tmem_ld_32x32b_x32(S + off, *reinterpret_cast<uint32_t(*)[32]>(r));
-            tmem_ld_32x32b_x32(S + off + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+            uint32_t r[32], w[16];
+            uint64_t pr[16];
+            tmem_ld_32x32b_x32(S + off, r);
             tmem_ld_wait();
-            uint64_t pr[32];
-            uint32_t w[32];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+            for (int e = 0; e < 16; e += 2) {
                 const ulonglong2 ls = *reinterpret_cast<const ulonglong2 *>(st + 2 * e);
 #pragma unroll
                 for (int k = e; k < e + 2; ++k) {
@@ -959,27 +969,26 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             if (edge) clear_edge(pr, first, end);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = pack_pair(pr[e]);
-            tmem_st_32x32b_x32(S + off, w);
+            for (int e = 0; e < 16; ++e) w[e] = pack_pair(pr[e]);
+            tmem_st_32x32b_x16(S + off, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(p_ready);
             if (!(ok = warp_all(mbar_wait(dp_full, n & 1)))) break;
             tc_fence_after();
-            tmem_ld_32x32b_x32(dP + off, *reinterpret_cast<uint32_t(*)[32]>(r));
-            tmem_ld_32x32b_x32(dP + off + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+            tmem_ld_32x32b_x32(dP + off, r);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
+            for (int e = 0; e < 16; e += 2) {
                 const ulonglong2 dl = *reinterpret_cast<const ulonglong2 *>(st + TILE + 2 * e);
                 pr[e] = f2_mul(pr[e], f2_add((uint64_t)r[2 * e + 1] << 32 | r[2 * e], dl.x));
                 pr[e + 1] = f2_mul(pr[e + 1], f2_add((uint64_t)r[2 * e + 3] << 32 | r[2 * e + 2], dl.y));
             }
             if (edge) clear_edge(pr, first, end);   // 0 times what is not finite
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = pack_pair(pr[e]);
-            tmem_st_32x32b_x32(dP + off, w);
+            for (int e = 0; e < 16; ++e) w[e] = pack_pair(pr[e]);
+            tmem_st_32x32b_x16(dP + off, w);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -989,17 +998,18 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         ok = ok && warp_all(mbar_wait(done, 0));
         if (ok) {
             tc_fence_after();
+            // dv by the first two warpgroups, dk by the others, half of the columns each
             const int k0 = t * TILE + (warp & 3) * 32;   // the warp's first key
-            const uint32_t cols = ((uint32_t)(warp & 3) << 21) + half * (D / 2);
-            const int64_t at = b + k0, col = (int64_t)g * D + half * (D / 2);
+            const uint32_t cols = ((uint32_t)(warp & 3) << 21) + (quarter & 1) * (D / 2);
+            const int64_t at = b + k0, col = (int64_t)g * D + (quarter & 1) * (D / 2);
             uint8_t *slab = sq + warp * 4096;            // the query tiles are no longer read
-            store_rows<D / 2>(dV + cols, 1.0f, slab, p.dv + at * p.lddv + col, p.lddv, len - k0, lane);
-            store_rows<D / 2>(dK + cols, p.scale, slab, p.dk + at * p.lddk + col, p.lddk, len - k0, lane);
+            if (quarter < 2) store_rows<D / 2>(dV + cols, 1.0f, slab, p.dv + at * p.lddv + col, p.lddv, len - k0, lane);
+            else store_rows<D / 2>(dK + cols, p.scale, slab, p.dk + at * p.lddk + col, p.lddk, len - k0, lane);
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 9) {
+    if (warp == GRAD_WARPS + 1) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -1098,7 +1108,7 @@ static pact_status run_bwd(const Params &p, cudaStream_t st) {
     s = launch_dep(dq::k_attn_dq<D>, dim3((unsigned)grid_q), dim3(SPLIT_THREADS), dq::Layout<D>::SMEM, st, what, q, g,
                    k, v, p, pairs);
     if (s != PACT_OK) return s;
-    return launch_dep(dkv::k_attn_dkv<D>, dim3((unsigned)grid_kv), dim3(SPLIT_THREADS), dkv::Layout<D>::SMEM, st, what,
+    return launch_dep(dkv::k_attn_dkv<D>, dim3((unsigned)grid_kv), dim3(GRAD_THREADS), dkv::Layout<D>::SMEM, st, what,
                       q, g, k, v, p, tiles);
 }
 
