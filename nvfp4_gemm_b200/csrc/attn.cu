@@ -99,6 +99,12 @@ __device__ __forceinline__ void mask_diagonal(uint32_t taddr, int row) {
     tmem_st_wait();
 }
 
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // D (+)= A(tmem) . B(smem)^T, BF16 x BF16 -> FP32, K = 16: the rows of A are tensor-memory
 // lanes, eight 32-bit columns hold its 16 BF16 values.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
@@ -529,11 +535,13 @@ namespace dq {
 template <int D>
 struct Layout {
     static constexpr int TILE_BYTES = D / 64 * BOX_BYTES;
-    static constexpr int SMEM = 1024 + 7 * TILE_BYTES + 256;   // Q0 Q1 dO0 dO1, K twice, V
+    static constexpr int DELTA = 7 * TILE_BYTES;                // Q0 Q1 dO0 dO1, K twice, V
+    static constexpr int BARS = DELTA + 2 * TILE * 4;           // delta of both units
+    static constexpr int SMEM = 1024 + BARS + 256;
 };
 
 template <int D>
-__global__ void __launch_bounds__(SPLIT_THREADS, 1)
+__global__ void __launch_bounds__(GRAD_THREADS, 1)
 k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
           const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p,
           const Slots sl) {
@@ -541,7 +549,8 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t *sk = smem + 4 * TB, *sv = smem + 6 * TB;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + 7 * TB);
+    float *s_delta = reinterpret_cast<float *>(smem + Layout<D>::DELTA);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Layout<D>::BARS);
     uint64_t *q_full = bars, *tail = bars + 1, *v_full = bars + 2, *v_empty = bars + 3, *k_full = bars + 4,
              *k_empty = bars + 6, *s_full = bars + 8, *s_read = bars + 10, *dp_full = bars + 12,
              *ds_ready = bars + 14, *dq_full = bars + 16;
@@ -549,7 +558,7 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 18; ++i) mbar_init(&bars[i], (i >= 10 && i < 12) || (i >= 14 && i < 16) ? 4 : 1);
+        for (int i = 0; i < 18; ++i) mbar_init(&bars[i], (i >= 10 && i < 12) || (i >= 14 && i < 16) ? GRAD_WARPS / 2 : 1);
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmG);
@@ -567,7 +576,7 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     const int t1 = two ? (int)((u0 + 1) / group) : t0, h1 = g * group + (int)((u0 + 1) % group);
     const int blocks = t1 + 1;
 
-    if (warp == 9) {
+    if (warp == GRAD_WARPS + 1) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
@@ -577,9 +586,9 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     // all 512 columns, from 0: two regions of 128, then dQ0, dQ1 (D each)
     constexpr uint32_t tmem = 0;
 
-    if (warp >= 8) {
-        regs_down();
-        if (warp == 8) {
+    if (warp >= GRAD_WARPS) {
+        grad_regs_down();
+        if (warp == GRAD_WARPS) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(q_full, (two ? 4 : 2) * TB);
                 load_tile<D>(smem, &tmQ, q_full, h0 * D, b + t0 * TILE);
@@ -620,7 +629,7 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             if (nk > 0) mbar_wait(&k_full[(nk - 1) & 1], ((nk - 1) >> 1) & 1);
             if (nk > 1) mbar_wait(&k_full[nk & 1], ((nk - 2) >> 1) & 1);
             if (nv > 0) mbar_wait(v_full, (nv - 1) & 1);
-        } else if (warp == 9 && elect_one()) {
+        } else if (warp == GRAD_WARPS + 1 && elect_one()) {
             const uint32_t base = smem_u32(smem), k0 = smem_u32(sk), v0 = smem_u32(sv);
             bool ok = mbar_wait(q_full, 0) && mbar_wait(&k_full[0], 0);
             tc_fence_after();
@@ -651,7 +660,7 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                     if (u ? !two : j > t0) continue;
                     if (!(ok = mbar_wait(&ds_ready[u], j & 1))) break;
                     tc_fence_after();
-                    mma_rows<D>(tmem + 2 * TILE + u * D, tmem + u * TILE, kj, j > 0);
+                    mma_quarters<D>(tmem + 2 * TILE + u * D, tmem + u * TILE, kj, j > 0);
                     if (j == (u ? t1 : t0)) {
                         tc_commit(&dq_full[u]);
                         continue;
@@ -668,90 +677,91 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             }
         }
     } else {
-        regs_up();
-        const int u = warp >> 2, row = threadIdx.x & 127, t = u ? t1 : t0, h = u ? h1 : h0;
-        const int last = u && !two ? -1 : t;
+        grad_regs_up();
+        const int u = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
+        const int t = u ? t1 : t0, h = u ? h1 : h0, last = u && !two ? -1 : t;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t X = tmem + u * TILE + lanes, Q = tmem + 2 * TILE + u * D + lanes;
-        const float c = p.scale * LOG2E;
-        const int q0 = t * TILE + (warp & 3) * 32;   // the warp's first query
+        const uint32_t X = tmem + u * TILE + half * 64 + lanes;   // this warp's lanes and half of the columns
+        const int q0 = t * TILE + (warp & 3) * 32;                // the warp's first query
         float delta = 0.0f, lse2 = 0.0f;
         if (last >= 0) {
-            // delta of the warp's 32 rows, D / 8 lanes a row (whole rows of o and do at a time),
-            // then from the lanes that summed a row to the lane that owns it
-            constexpr int L = D / 8, R = 32 / L;   // lanes a row, rows a load
+            const int64_t stat = (int64_t)h * p.M + b + q0 + lane;
+            if (q0 + lane < len) lse2 = p.lse[stat] * LOG2E;
+            // delta of 16 of the 32 rows (the other half's warp sums the rest), D / 8 lanes a row:
+            // whole rows of o and do at a time
+            constexpr int L = D / 8, R = 32 / L, N = 16 / R;   // lanes a row, rows a load, loads
             const pact_bf16 *po = p.o_in + (int64_t)h * D + (lane % L) * 8, *pd = p.dout + (int64_t)h * D + (lane % L) * 8;
-            float mine = 0.0f;
+            uint4 x[N], y[N];
 #pragma unroll
-            for (int i0 = 0; i0 < L; i0 += 8) {   // 16 loads in flight
-                uint4 x[8], y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = (i0 + i) * R + lane / L;
-                    const int64_t at = b + q0 + r;
-                    x[i] = y[i] = make_uint4(0, 0, 0, 0);
-                    if (q0 + r < len) {
-                        x[i] = *reinterpret_cast<const uint4 *>(po + at * p.ldo);
-                        y[i] = *reinterpret_cast<const uint4 *>(pd + at * p.lddo);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float u8[8], v8[8], s = 0.0f;
-                    unpack8_bf16(x[i], u8);
-                    unpack8_bf16(y[i], v8);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) s = fmaf(u8[e], v8[e], s);
-#pragma unroll
-                    for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                    if (lane % L == i0 + i) mine = s;   // row (i0 + i) R + lane / L
+            for (int i = 0; i < N; ++i) {
+                const int r = half * 16 + i * R + lane / L;
+                const int64_t at = b + q0 + r;
+                x[i] = y[i] = make_uint4(0, 0, 0, 0);
+                if (q0 + r < len) {
+                    x[i] = *reinterpret_cast<const uint4 *>(po + at * p.ldo);
+                    y[i] = *reinterpret_cast<const uint4 *>(pd + at * p.lddo);
                 }
             }
-            delta = __shfl_sync(0xffffffffu, mine, (lane % R) * L + lane / R);
-            if (q0 + lane < len) {
-                const int64_t stat = (int64_t)h * p.M + b + q0 + lane;
-                lse2 = p.lse[stat] * LOG2E;
+            float *sd = s_delta + u * TILE + (warp & 3) * 32;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float u8[8], v8[8], s = 0.0f;
+                unpack8_bf16(x[i], u8);
+                unpack8_bf16(y[i], v8);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(u8[e], v8[e], s);
+#pragma unroll
+                for (int o = L / 2; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (lane % L == 0) sd[half * 16 + i * R + lane / L] = s;
+            }
+            asm volatile("bar.sync %0, 256;" ::"r"(1 + u) : "memory");   // the unit's eight warps
+            delta = sd[lane];
+            if (half == 0 && q0 + lane < len) {
                 p.delta[stat] = delta;
                 p.lse2[stat] = lse2;
             }
         }
+        const float c = p.scale * LOG2E;
         const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-lse2, -lse2), d2 = f2_pack(-delta, -delta);
         bool ok = true;
         for (int j = 0; j <= last && ok; ++j) {
             if (!(ok = warp_all(mbar_wait(&s_full[u], j & 1)))) break;
             tc_fence_after();
-            uint32_t r[128];
-            tmem_ld_row(X, r);
+            uint32_t r[64];
+            tmem_ld_32x32b_x32(X, *reinterpret_cast<uint32_t(*)[32]>(r));
+            tmem_ld_32x32b_x32(X + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+            tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_read[u]);
-            uint64_t pr[64];
+            uint64_t pr[32];
 #pragma unroll
-            for (int e = 0; e < 64; ++e) {
+            for (int e = 0; e < 32; ++e) {
                 const uint64_t x = f2_fma((uint64_t)r[2 * e + 1] << 32 | r[2 * e], c2, m2);
                 pr[e] = e % EX2_PERIOD < EX2_BY_FMA_DQ ? ex2_fma(x) : ex2_pair(x);
             }
             if (!(ok = warp_all(mbar_wait(&dp_full[u], j & 1)))) break;
             tc_fence_after();
+            const int n = row - half * 64;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a[32], w[16];
-                tmem_ld_32x32b_x32(X + 32 * i, a);
+            for (int i = 0; i < 4; ++i) {   // 16 columns at a time: the registers hold no more
+                uint32_t a[16], w[8];
+                tmem_ld_32x32b_x16(X + 16 * i, a);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    pr[16 * i + e] = f2_mul(pr[16 * i + e], f2_add((uint64_t)a[2 * e + 1] << 32 | a[2 * e], d2));
+                for (int e = 0; e < 8; ++e)
+                    pr[8 * i + e] = f2_mul(pr[8 * i + e], f2_add((uint64_t)a[2 * e + 1] << 32 | a[2 * e], d2));
                 if (j == t) {   // the diagonal block: keys after the query
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < 8; ++e) {
                         float x, y;
-                        f2_unpack(pr[16 * i + e], x, y);
-                        pr[16 * i + e] = f2_pack(32 * i + 2 * e > row ? 0.0f : x, 32 * i + 2 * e + 1 > row ? 0.0f : y);
+                        f2_unpack(pr[8 * i + e], x, y);
+                        pr[8 * i + e] = f2_pack(16 * i + 2 * e > n ? 0.0f : x, 16 * i + 2 * e + 1 > n ? 0.0f : y);
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = pack_pair(pr[16 * i + e]);
-                tmem_st_32x32b_x16(X + 16 * i, w);
+                for (int e = 0; e < 8; ++e) w[e] = pack_pair(pr[8 * i + e]);
+                tmem_st_32x32b_x8(X + 32 * (i >> 1) + 8 * (i & 1), w);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -761,14 +771,16 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         ok = last >= 0 && ok && warp_all(mbar_wait(&dq_full[u], 0));
         if (ok) {
             tc_fence_after();
-            // the unit's Q tile is no longer read: its memory passes the output on
-            store_rows<D>(Q, p.scale, smem + u * TB + (warp & 3) * 4096,
-                          p.dq + (int64_t)(b + q0) * p.lddq + (int64_t)h * D, p.lddq, len - q0, lane);
+            // half of the columns each; the unit's Q and dO tiles are no longer read and pass the
+            // output on
+            const int col = half * (D / 2);
+            store_rows<D / 2>(tmem + 2 * TILE + u * D + col + lanes, p.scale, smem + (u + 2 * half) * TB + (warp & 3) * 4096,
+                              p.dq + (int64_t)(b + q0) * p.lddq + (int64_t)h * D + col, p.lddq, len - q0, lane);
         }
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 9) {
+    if (warp == GRAD_WARPS + 1) {
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, 512);
@@ -1105,7 +1117,7 @@ static pact_status run_bwd(const Params &p, cudaStream_t st) {
     const Slots pairs = pair_slots(p), tiles = {1, TILE, 1};
     const int64_t grid_q = pairs.first(p.M, p.nseq) * p.kv_heads, grid_kv = tiles.first(p.M, p.nseq) * p.kv_heads;
     PACT_CHECK(grid_q <= 0x7FFFFFFF && grid_kv <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many tiles", what);
-    s = launch_dep(dq::k_attn_dq<D>, dim3((unsigned)grid_q), dim3(SPLIT_THREADS), dq::Layout<D>::SMEM, st, what, q, g,
+    s = launch_dep(dq::k_attn_dq<D>, dim3((unsigned)grid_q), dim3(GRAD_THREADS), dq::Layout<D>::SMEM, st, what, q, g,
                    k, v, p, pairs);
     if (s != PACT_OK) return s;
     return launch_dep(dkv::k_attn_dkv<D>, dim3((unsigned)grid_kv), dim3(GRAD_THREADS), dkv::Layout<D>::SMEM, st, what,
