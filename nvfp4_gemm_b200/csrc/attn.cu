@@ -516,14 +516,13 @@ __device__ __forceinline__ void grad_regs_up() { asm volatile("setmaxnreg.inc.sy
 __device__ __forceinline__ void grad_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
 static_assert(512 * 104 + 128 * 64 <= GRAD_THREADS * 96, "more registers than the block is launched with");
 
-// tmem (+)= A . Y: the four 32-row quarters of A's contraction lie 32 columns apart, each over the
-// first half of the 32 FP32 columns it was computed from.
-template <int D>
-__device__ __forceinline__ void mma_quarters(uint32_t tmem, uint32_t a, uint32_t y, bool accumulate) {
+// tmem (+)= A . Y over steps [S0, S1) of 16 contraction rows: the BF16 values of a step (8 columns)
+// lie over the first half of the 16 FP32 columns they were computed from.
+template <int D, int S0, int S1>
+__device__ __forceinline__ void mma_spread(uint32_t tmem, uint32_t a, uint32_t y, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16(TILE, D, false, true);
 #pragma unroll
-    for (int s = 0; s < TILE / 16; ++s)
-        mma_bf16_ts(tmem, a + (s >> 1) * 32 + (s & 1) * 8, desc_rows(y, s), idesc, accumulate || s > 0);
+    for (int s = S0; s < S1; ++s) mma_bf16_ts(tmem, a + 16 * s, desc_rows(y, s), idesc, accumulate || s > 0);
 }
 __device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
     float x, y;
@@ -552,13 +551,13 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     float *s_delta = reinterpret_cast<float *>(smem + Layout<D>::DELTA);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Layout<D>::BARS);
     uint64_t *q_full = bars, *tail = bars + 1, *v_full = bars + 2, *v_empty = bars + 3, *k_full = bars + 4,
-             *k_empty = bars + 6, *s_full = bars + 8, *s_read = bars + 10, *dp_full = bars + 12,
-             *ds_ready = bars + 14, *dq_full = bars + 16;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 18);
+             *k_empty = bars + 6, *s_full = bars + 8, *dp_full = bars + 10, *dq_full = bars + 12,
+             *s_read = bars + 14, *ds_ready = bars + 16;   // ds_ready: [unit][keys 0-63, 64-127]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 20);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 18; ++i) mbar_init(&bars[i], (i >= 10 && i < 12) || (i >= 14 && i < 16) ? GRAD_WARPS / 2 : 1);
+        for (int i = 0; i < 20; ++i) mbar_init(&bars[i], i >= 14 ? GRAD_WARPS / 2 : 1);
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmG);
@@ -658,9 +657,12 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     if (u ? !two : j > t0) continue;
-                    if (!(ok = mbar_wait(&ds_ready[u], j & 1))) break;
+                    if (!(ok = mbar_wait(&ds_ready[2 * u], j & 1))) break;
                     tc_fence_after();
-                    mma_quarters<D>(tmem + 2 * TILE + u * D, tmem + u * TILE, kj, j > 0);
+                    mma_spread<D, 0, 4>(tmem + 2 * TILE + u * D, tmem + u * TILE, kj, j > 0);
+                    if (!(ok = mbar_wait(&ds_ready[2 * u + 1], j & 1))) break;
+                    tc_fence_after();
+                    mma_spread<D, 4, 8>(tmem + 2 * TILE + u * D, tmem + u * TILE, kj, true);
                     if (j == (u ? t1 : t0)) {
                         tc_commit(&dq_full[u]);
                         continue;
@@ -681,7 +683,8 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         const int u = warp >> 3, half = (warp >> 2) & 1, row = threadIdx.x & 127;
         const int t = u ? t1 : t0, h = u ? h1 : h0, last = u && !two ? -1 : t;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t X = tmem + u * TILE + half * 64 + lanes;   // this warp's lanes and half of the columns
+        // this warp's lanes; its columns are 32 half .. + 31 of both 64-key halves of a block
+        const uint32_t X = tmem + u * TILE + half * 32 + lanes;
         const int q0 = t * TILE + (warp & 3) * 32;                // the warp's first query
         float delta = 0.0f, lse2 = 0.0f;
         if (last >= 0) {
@@ -729,7 +732,7 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             tc_fence_after();
             uint32_t r[64];
             tmem_ld_32x32b_x32(X, *reinterpret_cast<uint32_t(*)[32]>(r));
-            tmem_ld_32x32b_x32(X + 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
+            tmem_ld_32x32b_x32(X + 64, *reinterpret_cast<uint32_t(*)[32]>(r + 32));
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
@@ -742,11 +745,12 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             }
             if (!(ok = warp_all(mbar_wait(&dp_full[u], j & 1)))) break;
             tc_fence_after();
-            const int n = row - half * 64;
+            const int n = row - half * 32;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {   // 16 columns at a time: the registers hold no more
+                const int c0 = 64 * (i >> 1) + 16 * (i & 1);
                 uint32_t a[16], w[8];
-                tmem_ld_32x32b_x16(X + 16 * i, a);
+                tmem_ld_32x32b_x16(X + c0, a);
                 tmem_ld_wait();
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -756,17 +760,19 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                     for (int e = 0; e < 8; ++e) {
                         float x, y;
                         f2_unpack(pr[8 * i + e], x, y);
-                        pr[8 * i + e] = f2_pack(16 * i + 2 * e > n ? 0.0f : x, 16 * i + 2 * e + 1 > n ? 0.0f : y);
+                        pr[8 * i + e] = f2_pack(c0 + 2 * e > n ? 0.0f : x, c0 + 2 * e + 1 > n ? 0.0f : y);
                     }
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = pack_pair(pr[8 * i + e]);
-                tmem_st_32x32b_x8(X + 32 * (i >> 1) + 8 * (i & 1), w);
+                tmem_st_32x32b_x8(X + c0, w);
+                if (i & 1) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ds_ready[2 * u + (i >> 1)]);
+                }
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_ready[u]);
         }
         ok = last >= 0 && ok && warp_all(mbar_wait(&dq_full[u], 0));
         if (ok) {
@@ -807,9 +813,9 @@ struct Layout {
 };
 
 // Pairs of a masked tile: columns before `first` or from `end` on become zero.
-__device__ __forceinline__ void clear_edge(uint64_t (&v)[16], int first, int end) {
+__device__ __forceinline__ void clear_edge(uint64_t (&v)[8], int first, int end) {
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < 8; ++e) {
         float x, y;
         f2_unpack(v[e], x, y);
         if (2 * e < first || 2 * e >= end) x = 0.0f;
@@ -818,11 +824,59 @@ __device__ __forceinline__ void clear_edge(uint64_t (&v)[16], int first, int end
     }
 }
 
+// The group's query heads over a cluster of `ns` CTAs: each left its FP32 sums (dv, dk: [128 x D],
+// 16-byte chunk c of row r at c ^ (r % 8)) in its own shared memory at `part`; CTA `rank` adds its
+// share of the rows over the CTAs in order and stores them.
+template <int D>
+__device__ __forceinline__ void join(const Params &p, uint32_t part, int ns, int rank, int b, int len, int t, int g) {
+    constexpr int CH = D / 8;   // 8 columns a thread
+    const int rows = TILE / ns;
+    for (int i = threadIdx.x; i < 2 * rows * CH; i += GRAD_THREADS) {
+        const int c = i % CH, r = rank * rows + i / CH % rows, kj = t * TILE + r;
+        const bool is_k = i / (CH * rows) != 0;
+        if (kj >= len) continue;
+        float v[8] = {};
+        for (int q = 0; q < ns; ++q) {
+            const uint32_t base = mapa_shared(part + ((is_k ? TILE : 0) + r) * D * 4, q);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float x[4];
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                             : "r"(base + (((2 * c + h) ^ (r & 7)) << 4))
+                             : "memory");
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * h + e] += x[e];
+            }
+        }
+        const float f = is_k ? p.scale : 1.0f;
+        pact_bf16 *dst = (is_k ? p.dk + (int64_t)(b + kj) * p.lddk : p.dv + (int64_t)(b + kj) * p.lddv) + (int64_t)g * D + 8 * c;
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(v[0] * f, v[1] * f), pack_bf16x2(v[2] * f, v[3] * f),
+                                                     pack_bf16x2(v[4] * f, v[5] * f), pack_bf16x2(v[6] * f, v[7] * f));
+    }
+}
+// N accumulator columns of a lane to columns col .. of its row of `part`.
+template <int D, int N>
+__device__ __forceinline__ void leave(uint32_t taddr, uint32_t part, int row, int col) {
+#pragma unroll
+    for (int i = 0; i < N; i += 16) {
+        uint32_t a[16];
+        tmem_ld_32x32b_x16(taddr + i, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             part + row * D * 4 + ((((col + i + e) >> 2) ^ (row & 7)) << 4)),
+                         "r"(a[e]), "r"(a[e + 1]), "r"(a[e + 2]), "r"(a[e + 3])
+                         : "memory");
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(GRAD_THREADS, 1)
 k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmG,
            const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const Params p,
-           const Slots sl) {
+           const Slots sl, const int ns) {
     constexpr int TB = Layout<D>::TILE_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -830,13 +884,13 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     float *stats = reinterpret_cast<float *>(smem + Layout<D>::STATS);   // [unit & 1][-lse2, -delta][128]
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + Layout<D>::BARS);
     uint64_t *kv_full = bars, *tail = bars + 1, *q_full = bars + 2, *q_empty = bars + 4, *g_full = bars + 6,
-             *g_empty = bars + 8, *s_full = bars + 10, *p_ready = bars + 11, *dp_full = bars + 12,
-             *ds_ready = bars + 13, *done = bars + 14;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 15);
+             *g_empty = bars + 8, *s_full = bars + 10, *dp_full = bars + 11, *done = bars + 12,
+             *p_ready = bars + 13, *ds_ready = bars + 15;   // queries 0-63 of a tile, 64-127
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + 17);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 15; ++i) mbar_init(&bars[i], i == 11 || i == 13 ? GRAD_WARPS : i == 2 || i == 3 ? 2 : 1);
+        for (int i = 0; i < 17; ++i) mbar_init(&bars[i], i >= 13 ? GRAD_WARPS : i == 2 || i == 3 ? 2 : 1);
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmG);
@@ -844,12 +898,14 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         prefetch_tensormap(&tmV);
     }
     pdl_wait();
-    const int g = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
+    const int rank = blockIdx.x % ns, cluster = blockIdx.x / ns;   // the cluster's CTAs take every ns-th head
+    const int g = cluster % p.kv_heads, group = p.heads / p.kv_heads;
     int b, len, t;
-    find_slot(p, sl, blockIdx.x / p.kv_heads, lane, &b, &len, &t);
+    find_slot(p, sl, cluster / p.kv_heads, lane, &b, &len, &t);
     const int tiles = (len + TILE - 1) / TILE;
-    if (t >= tiles) return;   // block-uniform, before tensor memory is allocated
-    const int units = (tiles - t) * group;   // unit n: query tile t + n / group, head n % group of the group
+    if (t >= tiles) return;   // cluster-uniform, before tensor memory is allocated
+    const int heads = (group - rank + ns - 1) / ns;
+    const int units = (tiles - t) * heads;   // unit n: query tile t + n / heads, head rank + n % heads ns of the group
 
     if (warp == GRAD_WARPS + 1) {
         tmem_alloc(tmem_slot, 512);
@@ -871,7 +927,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             int n = 0, tails = 0, i = t, hh = 0;
             for (; n < units; ++n) {
-                const int s = n & 1, par = ((n >> 1) & 1) ^ 1, h = g * group + hh, row = b + i * TILE;
+                const int s = n & 1, par = ((n >> 1) & 1) ^ 1, h = g * group + rank + hh * ns, row = b + i * TILE;
                 const int rows = len - i * TILE;
                 uint8_t *dq_ = sq + s * TB, *dg = sg + s * TB;
                 const bool partial = rows < TILE;   // the sequence's last query tile
@@ -903,7 +959,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                         mbar_arrive(&g_full[s]);
                     }
                 }
-                if (++hh == group) { hh = 0; ++i; }
+                if (++hh == heads) { hh = 0; ++i; }
             }
             // every copy lands before the CTA may leave
             mbar_wait(kv_full, 0);
@@ -928,9 +984,12 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             for (int n = 0; n < units && ok; ++n) {
                 const int s = n & 1, s1 = s ^ 1, par1 = ((n + 1) >> 1) & 1;
                 const bool more = n + 1 < units;
-                if (!(ok = mbar_wait(p_ready, n & 1))) break;
+                if (!(ok = mbar_wait(&p_ready[0], n & 1))) break;
                 tc_fence_after();
-                mma_quarters<D>(dV, S, g0 + s * TB, n > 0);
+                mma_spread<D, 0, 4>(dV, S, g0 + s * TB, n > 0);
+                if (!(ok = mbar_wait(&p_ready[1], n & 1))) break;
+                tc_fence_after();
+                mma_spread<D, 4, 8>(dV, S, g0 + s * TB, true);
                 tc_commit(&g_empty[s]);
                 if (more) {
                     if (!(ok = mbar_wait(&q_full[s1], par1))) break;
@@ -938,9 +997,12 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     mma_cols<D>(S, k0, q0 + s1 * TB);
                     tc_commit(s_full);
                 }
-                if (!(ok = mbar_wait(ds_ready, n & 1))) break;
+                if (!(ok = mbar_wait(&ds_ready[0], n & 1))) break;
                 tc_fence_after();
-                mma_quarters<D>(dK, dP, q0 + s * TB, n > 0);
+                mma_spread<D, 0, 4>(dK, dP, q0 + s * TB, n > 0);
+                if (!(ok = mbar_wait(&ds_ready[1], n & 1))) break;
+                tc_fence_after();
+                mma_spread<D, 4, 8>(dK, dP, q0 + s * TB, true);
                 tc_commit(&q_empty[s]);
                 if (more) {
                     if (!(ok = mbar_wait(&g_full[s1], par1))) break;
@@ -954,73 +1016,96 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     } else {
         grad_regs_up();
         const int quarter = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t off = ((uint32_t)(warp & 3) << 21) + quarter * 32;   // this warp's lanes and columns
+        // this warp's lanes; its columns are 16 quarter .. + 15 of both halves of a tile, so that the
+        // first half of P, dS is ready early and the products start on it
+        const uint32_t off = ((uint32_t)(warp & 3) << 21) + quarter * 16;
         const uint64_t c2 = f2_pack(p.scale * LOG2E, p.scale * LOG2E);
         bool ok = true;
         int i = t, hh = 0;
         for (int n = 0; n < units; ++n) {
-            const float *st = stats + (n & 1) * 2 * TILE + quarter * 32;
+            const float *st = stats + (n & 1) * 2 * TILE + quarter * 16;
             // a masked pair: the query is before the key, or behind the sequence
-            const int first = i == t ? row - quarter * 32 : 0, end = len - i * TILE - quarter * 32;
-            const bool edge = i == t || end < 32;
+            const int first = i == t ? row - quarter * 16 : 0, end = len - i * TILE - quarter * 16;
+            const bool edge = i == t || end < 80;
             if (!(ok = warp_all(mbar_wait(&q_full[n & 1], (n >> 1) & 1)))) break;   // the statistics
             if (!(ok = warp_all(mbar_wait(s_full, n & 1)))) break;
             tc_fence_after();
-            uint32_t r[32], w[16];
-            uint64_t pr[16];
-            tmem_ld_32x32b_x32(S + off, r);
+            uint32_t r[2][16];
+            uint64_t pr[2][8];
+            tmem_ld_32x32b_x16(S + off, r[0]);
+            tmem_ld_32x32b_x16(S + off + 64, r[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const ulonglong2 ls = *reinterpret_cast<const ulonglong2 *>(st + 2 * e);
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t w[8];
 #pragma unroll
-                for (int k = e; k < e + 2; ++k) {
-                    const uint64_t x = f2_fma((uint64_t)r[2 * k + 1] << 32 | r[2 * k], c2, k == e ? ls.x : ls.y);
-                    pr[k] = k % EX2_PERIOD < EX2_BY_FMA_DKV ? ex2_fma(x) : ex2_pair(x);
+                for (int e = 0; e < 8; e += 2) {
+                    const ulonglong2 ls = *reinterpret_cast<const ulonglong2 *>(st + 64 * hf + 2 * e);
+#pragma unroll
+                    for (int k = e; k < e + 2; ++k) {
+                        const uint64_t x = f2_fma((uint64_t)r[hf][2 * k + 1] << 32 | r[hf][2 * k], c2, k == e ? ls.x : ls.y);
+                        pr[hf][k] = k % EX2_PERIOD < EX2_BY_FMA_DKV ? ex2_fma(x) : ex2_pair(x);
+                    }
                 }
-            }
-            if (edge) clear_edge(pr, first, end);
+                if (edge) clear_edge(pr[hf], first - 64 * hf, end - 64 * hf);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pack_pair(pr[e]);
-            tmem_st_32x32b_x16(S + off, w);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_ready);
+                for (int e = 0; e < 8; ++e) w[e] = pack_pair(pr[hf][e]);
+                tmem_st_32x32b_x8(S + off + 64 * hf, w);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[hf]);
+            }
             if (!(ok = warp_all(mbar_wait(dp_full, n & 1)))) break;
             tc_fence_after();
-            tmem_ld_32x32b_x32(dP + off, r);
+            tmem_ld_32x32b_x16(dP + off, r[0]);
+            tmem_ld_32x32b_x16(dP + off + 64, r[1]);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const ulonglong2 dl = *reinterpret_cast<const ulonglong2 *>(st + TILE + 2 * e);
-                pr[e] = f2_mul(pr[e], f2_add((uint64_t)r[2 * e + 1] << 32 | r[2 * e], dl.x));
-                pr[e + 1] = f2_mul(pr[e + 1], f2_add((uint64_t)r[2 * e + 3] << 32 | r[2 * e + 2], dl.y));
-            }
-            if (edge) clear_edge(pr, first, end);   // 0 times what is not finite
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t w[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = pack_pair(pr[e]);
-            tmem_st_32x32b_x16(dP + off, w);
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(ds_ready);
-            if (++hh == group) { hh = 0; ++i; }
+                for (int e = 0; e < 8; e += 2) {
+                    const ulonglong2 dl = *reinterpret_cast<const ulonglong2 *>(st + TILE + 64 * hf + 2 * e);
+                    pr[hf][e] = f2_mul(pr[hf][e], f2_add((uint64_t)r[hf][2 * e + 1] << 32 | r[hf][2 * e], dl.x));
+                    pr[hf][e + 1] = f2_mul(pr[hf][e + 1], f2_add((uint64_t)r[hf][2 * e + 3] << 32 | r[hf][2 * e + 2], dl.y));
+                }
+                if (edge) clear_edge(pr[hf], first - 64 * hf, end - 64 * hf);   // 0 times what is not finite
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = pack_pair(pr[hf][e]);
+                tmem_st_32x32b_x8(dP + off + 64 * hf, w);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ds_ready[hf]);
+            }
+            if (++hh == heads) { hh = 0; ++i; }
         }
         ok = ok && warp_all(mbar_wait(done, 0));
         if (ok) {
             tc_fence_after();
             // dv by the first two warpgroups, dk by the others, half of the columns each
-            const int k0 = t * TILE + (warp & 3) * 32;   // the warp's first key
-            const uint32_t cols = ((uint32_t)(warp & 3) << 21) + (quarter & 1) * (D / 2);
-            const int64_t at = b + k0, col = (int64_t)g * D + (quarter & 1) * (D / 2);
-            uint8_t *slab = sq + warp * 4096;            // the query tiles are no longer read
-            if (quarter < 2) store_rows<D / 2>(dV + cols, 1.0f, slab, p.dv + at * p.lddv + col, p.lddv, len - k0, lane);
-            else store_rows<D / 2>(dK + cols, p.scale, slab, p.dk + at * p.lddk + col, p.lddk, len - k0, lane);
+            const int k0 = t * TILE + (warp & 3) * 32, c0 = (quarter & 1) * (D / 2);   // the warp's first key
+            const uint32_t acc = (quarter < 2 ? dV : dK) + ((uint32_t)(warp & 3) << 21) + c0;
+            if (ns > 1) {
+                leave<D, D / 2>(acc, smem_u32(sq) + (quarter < 2 ? 0 : TILE * D * 4), row, c0);
+            } else {
+                const int64_t at = b + k0, col = (int64_t)g * D + c0;
+                uint8_t *slab = sq + warp * 4096;   // the query tiles are no longer read
+                if (quarter < 2) store_rows<D / 2>(acc, 1.0f, slab, p.dv + at * p.lddv + col, p.lddv, len - k0, lane);
+                else store_rows<D / 2>(acc, p.scale, slab, p.dk + at * p.lddk + col, p.lddk, len - k0, lane);
+            }
         }
         tc_fence_before();
     }
     __syncthreads();
+    if (ns > 1) {
+        __syncwarp();
+        cluster_sync();
+        join<D>(p, smem_u32(sq), ns, rank, b, len, t, g);
+        __syncwarp();
+        cluster_sync();   // no CTA leaves while another reads its sums
+    }
     if (warp == GRAD_WARPS + 1) {
         __syncwarp();
         tc_fence_after();
@@ -1120,8 +1205,31 @@ static pact_status run_bwd(const Params &p, cudaStream_t st) {
     s = launch_dep(dq::k_attn_dq<D>, dim3((unsigned)grid_q), dim3(GRAD_THREADS), dq::Layout<D>::SMEM, st, what, q, g,
                    k, v, p, pairs);
     if (s != PACT_OK) return s;
-    return launch_dep(dkv::k_attn_dkv<D>, dim3((unsigned)grid_kv), dim3(GRAD_THREADS), dkv::Layout<D>::SMEM, st, what,
-                      q, g, k, v, p, tiles);
+    // A key tile's CTA runs over all later query tiles of the group's heads.  Where there are fewer key
+    // tiles than SMs, the heads are spread over a cluster of CTAs that add their sums at the end,
+    // for some 5 us.  Gradients over 1999 tokens, 32 and 8 heads of 64 (128 tiles): 137 us with one
+    // CTA a tile, 106 with two, 136 with four; 2048 tokens, 12 and 2 heads of 128 (32 tiles): 193, 128,
+    // 107; 8192 tokens, 24 and 8 heads of 128 (512 tiles): 343, 446 with two.
+    const int group = p.heads / p.kv_heads;
+    int ns = 1;
+    while (2 * ns <= group && ns < 8 && ns * (int64_t)(p.M / TILE + 1) * p.kv_heads < sm_count()) ns *= 2;
+    PACT_CHECK(grid_kv * ns <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many tiles", what);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid_kv * ns));
+    cfg.blockDim = dim3(GRAD_THREADS);
+    cfg.dynamicSmemBytes = dkv::Layout<D>::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ns;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, dkv::k_attn_dkv<D>, q, g, k, v, p, tiles, ns);
+    PACT_CHECK(e == cudaSuccess, PACT_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(e));
+    return launch_status(what);
 }
 
 }  // namespace attn
