@@ -28,7 +28,7 @@
 namespace pact {
 namespace muon {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int BATCH = 128;     // matrices per launch: their descriptors are kernel parameters
 constexpr int STEPS = 5;
@@ -44,14 +44,15 @@ __host__ __device__ constexpr size_t stage_smem(int nb) { return sizeof(float) *
 __host__ __device__ constexpr size_t gram_smem(int nb) { return stage_smem(nb) + sizeof(double) * WARPS * 64; }
 __host__ __device__ constexpr size_t apply_smem(int nb) { return stage_smem(nb) + sizeof(double) * mat_size(nb); }
 __host__ __device__ constexpr size_t poly_smem(int nb) { return sizeof(double) * 5 * mat_size(nb); }
-// The fused kernel: slab, the CTA's part of the Gram matrix (also the warps' exchange), the five matrices.
+// The fused kernel: slab, the CTA's part of the Gram matrix, the five matrices (first the warps' exchange).
 __host__ __device__ constexpr size_t fused_smem(int nb, int len) {
-    return sizeof(float) * 8 * nb * ((len + 31) / 32 * 32 + 8) + sizeof(double) * (tri(nb) * 64 + WARPS * 64) + poly_smem(nb);
+    return sizeof(float) * 8 * nb * ((len + 31) / 32 * 32 + 8) + sizeof(double) * tri(nb) * 64 + poly_smem(nb);
 }
-constexpr size_t FUSED_FIRST = 74 * 1024;    // three CTAs an SM
+constexpr size_t FUSED_FIRST = 110 * 1024;   // two CTAs an SM
 constexpr size_t FUSED_MOST = 226 * 1024;
 constexpr int FUSED_NB = 6;                  // beyond, the FP64 matrices leave no room for a slab
 constexpr int CLUSTER = 8;
+static_assert(WARPS * 64 <= 5 * mat_size(2), "the warps exchange their sums where the matrices come to lie");
 
 struct Matrix {
     const void *grad;
@@ -273,9 +274,9 @@ __device__ __forceinline__ void update_w(const Params &p, const Matrix &a, int k
 // The slab's part of u u^T, summed over the warps in order: the upper 8 x 8 blocks, as the lanes of the
 // FP64 tensor instruction hold them, to out[tri x 64].  The fragments of both operands of a block of a
 // symmetric product are the same registers (row lane / 4, position lane % 4).
-template <int NB>
-__device__ __forceinline__ void gram(const float *us, int ld, int n8, double *sum, double *out) {
-    constexpr int T = tri(NB);
+template <int NB, int B0, int B1>   // block rows [B0, B1) of the triangle
+__device__ __forceinline__ void gram_rows(const float *us, int ld, int n8, double *sum, double *out) {
+    constexpr int T0 = tri(NB) - tri(NB - B0), T = tri(NB) - tri(NB - B1) - T0;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     double acc[T][2] = {};
     for (int k = warp * 8; k < n8; k += WARPS * 8) {
@@ -283,10 +284,10 @@ __device__ __forceinline__ void gram(const float *us, int ld, int n8, double *su
         for (int h = 0; h < 8; h += 4) {
             double f[NB];
 #pragma unroll
-            for (int b = 0; b < NB; ++b) f[b] = (double)us[(8 * b + (lane >> 2)) * ld + k + h + (lane & 3)];
+            for (int b = B0; b < NB; ++b) f[b] = (double)us[(8 * b + (lane >> 2)) * ld + k + h + (lane & 3)];
             int t = 0;
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = B0; b < B1; ++b)
 #pragma unroll
                 for (int c = b; c < NB; ++c) dmma(acc[t++], f[b], f[c]);
         }
@@ -302,9 +303,18 @@ __device__ __forceinline__ void gram(const float *us, int ld, int n8, double *su
         if (threadIdx.x < 64) {
             double s = 0.0;
             for (int w = 0; w < WARPS; ++w) s += sum[w * 64 + threadIdx.x];
-            out[t * 64 + threadIdx.x] = s;
+            out[(T0 + t) * 64 + threadIdx.x] = s;
         }
         __syncthreads();
+    }
+}
+template <int NB>
+__device__ __forceinline__ void gram(const float *us, int ld, int n8, double *sum, double *out) {
+    if constexpr (NB <= 6) {
+        gram_rows<NB, 0, NB>(us, ld, n8, sum, out);
+    } else {   // the 36 blocks of r = 64 exceed the registers: 21 and 15
+        gram_rows<NB, 0, 3>(us, ld, n8, sum, out);
+        gram_rows<NB, 3, NB>(us, ld, n8, sum, out);
     }
 }
 
@@ -451,7 +461,7 @@ __global__ void __launch_bounds__(THREADS) k_muon_apply(const __grid_constant__ 
 // matrix in order through distributed shared memory, and each forms P (the same bits) for its
 // own slab.
 template <int NB>
-__global__ void __launch_bounds__(THREADS) k_muon_fused(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(THREADS, NB == 2 ? 2 : 1) k_muon_fused(const __grid_constant__ Params p) {
     constexpr int T = tri(NB);
     extern __shared__ __align__(16) float us[];
     pdl_wait();
@@ -467,11 +477,11 @@ __global__ void __launch_bounds__(THREADS) k_muon_fused(const __grid_constant__ 
     to_matrix(p, a, idle ? 0 : j);
     const int ld = (a.slab + 31) / 32 * 32 + 8, k0 = rank * a.slab, n = idle ? 0 : max(0, min(a.slab, a.len - k0));
     const int n8 = (n + 7) & ~7;
-    double *part = reinterpret_cast<double *>(us + 8 * NB * ld), *sum = part + T * 64, *sm = sum + WARPS * 64;
+    double *part = reinterpret_cast<double *>(us + 8 * NB * ld), *sm = part + T * 64;
     clear_rest<NB>(a, n, n8, us, ld);
     stage_u<true>(p, a, k0, n, us, ld);
     __syncthreads();
-    gram<NB>(us, ld, n8, sum, part);
+    gram<NB>(us, ld, n8, sm, part);
     if (a.ctas > 1) cluster_sync();
     const uint32_t mine = smem_u32(part), first = cluster_ctarank() / a.ctas * a.ctas;
     const double *P = polynomial<NB>(a, sm, [&](int t) {
@@ -641,7 +651,7 @@ pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32,
         a.vec = al && m.cols % 4 == 0 ? 4 : 1;
         return a;
     };
-    // The matrices that fit a cluster's shared memory: as few CTAs each as leave three CTAs room on an SM
+    // The matrices that fit a cluster's shared memory: as few CTAs each as leave two CTAs room on an SM
     // (or, in clusters of eight, as fit at all), more while the SMs are not all busy.
     int64_t fused = 0;
     for (int first = 0; first < n && nb <= muon::FUSED_NB; first += BATCH) {

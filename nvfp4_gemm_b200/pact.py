@@ -628,6 +628,8 @@ def pact_rmsnorm_bwd(dy: torch.Tensor, yq: NVFP4Tensor, rstd: torch.Tensor, gamm
 
 def _on(t: torch.Tensor, name: str, dtype, dev: int, shape=None) -> torch.Tensor:
     """t is a tensor of this type and shape on device `dev`, the current one (where the call launches)."""
+    if t.dtype is dtype and t.get_device() == dev >= 0 and (shape is None or t.shape == shape):
+        return t
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA {str(dtype).replace('torch.', '')} tensor")
     if t.get_device() != dev:
@@ -771,7 +773,8 @@ def _muon_matrices(weights, grads, momenta, weights_out, momenta_out, weights_bf
                             (wo, "weights_out", f32), (w16, "weights_bf16", torch.bfloat16)):
             if t is None or (t is m and name == "momenta_out") or (t is w and name == "weights_out"):
                 continue
-            _on(t, name, dt, dev, shape)
+            if not (t.dtype is dt and t.get_device() == dev >= 0 and t.shape == shape):
+                _on(t, f"{name}[{i}]", dt, dev, shape)
             if not t.is_contiguous():
                 raise ValueError(f"{name}[{i}]: expected a contiguous tensor")
         mats[i] = (g.data_ptr(), m.data_ptr(), mo.data_ptr(), w.data_ptr(), wo.data_ptr(),
