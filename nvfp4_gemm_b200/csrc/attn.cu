@@ -224,9 +224,9 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t *sla
 // grid depends on M and nseq alone, and a slot finds its sequence by searching
 // seq_start, without a prefix sum over the sequences.
 struct Slots {
-    int64_t group, per;
-    int extra;
-    __host__ __device__ int64_t first(int64_t start, int64_t s) const { return start * group / per + s * extra; }
+    int64_t group;
+    int shift, extra;   // per = 1 << shift
+    __host__ __device__ int64_t first(int64_t start, int64_t s) const { return (start * group >> shift) + s * extra; }
 };
 
 // The sequence of work slot `slot`: rows [b, b + len) and the slot's number inside it;
@@ -247,6 +247,66 @@ __device__ __forceinline__ void find_slot(const Params &p, const Slots &sl, int6
     *len = max(start(lo + 1) - *b, 0);
     const int64_t it = slot - sl.first(*b, lo);
     *item = it < 0 || it > 0x7FFFFFFF ? 0x7FFFFFFF : (int)it;
+}
+
+// Work item `it` of `items` (slots times key heads), in order of falling slots (a sequence's last and
+// longest tiles first), the key heads of a slot side by side: a pair of units of one key head,
+// query tiles t0, t1 of heads h0, h1 (t1 = t0 where there is no second).
+struct Pair {
+    int b, len, g, t0, t1, h0, h1;
+    bool any, two;
+};
+__device__ __forceinline__ Pair find_pair(const Params &p, const Slots &sl, int it, int items, int lane) {
+    Pair w;
+    int item;
+    w.g = it % p.kv_heads;
+    find_slot(p, sl, items / p.kv_heads - 1 - it / p.kv_heads, lane, &w.b, &w.len, &item);
+    const int group = p.heads / p.kv_heads;
+    // (check() keeps tiles times heads below 2^31)
+    const uint32_t units = (uint32_t)((w.len + TILE - 1) / TILE) * group, u = 2 * (uint32_t)min(item, 0x3FFFFFFF);
+    w.any = u < units;
+    w.two = u + 1 < units;
+    w.t0 = u / group;
+    const int hh = u - w.t0 * group;
+    w.h0 = w.g * group + hh;
+    w.t1 = w.t0 + (w.two && hh + 1 == group);
+    w.h1 = w.g * group + (hh + 1 == group ? 0 : hh + 1);
+    return w;
+}
+
+// Dynamic scheduling: a grid has a CTA for every work item, and a running CTA that runs out of work cancels
+// the launch of the next pending one and takes over its item (clusterlaunchcontrol).  The
+// items differ by a factor of 16 in length; handed out in turn they left the slowest SM
+// with 58 blocks of 43 on average.
+__device__ __forceinline__ void request_item(uint4 *response, uint64_t *bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(response)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The cancelled CTA's number, or -1 where none was left.
+__device__ __forceinline__ int answered_item(const uint4 *response) {
+    uint32_t x = 0, got;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %1, 1, 0, p;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, _, _, _}, r;\n\t}"
+        : "+r"(x), "=r"(got)
+        : "r"(smem_u32(response))
+        : "memory");
+    return got ? (int)x : -1;
+}
+// A warp's next item: the n-th answer, from two slots in turn; `read` learns that the warp has read it.
+__device__ __forceinline__ int next_item(const uint4 *responses, uint64_t *answered, uint64_t *read, int n, int lane) {
+    if (!warp_all(mbar_wait(&answered[n & 1], (n >> 1) & 1))) return -1;
+    const int it = answered_item(&responses[n & 1]);
+    fence_proxy_async_smem();   // the next answer is written by the async proxy
+    __syncwarp();
+    if (read && lane == 0) mbar_arrive(&read[n & 1]);
+    return it;
 }
 
 constexpr int SPLIT_THREADS = 384;   // three warpgroups; registers are moved to the first two
@@ -274,7 +334,7 @@ constexpr int STAGES = 4;
 template <int D>
 struct Layout {
     static constexpr int TILE_BYTES = D / 64 * BOX_BYTES;
-    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE_BYTES + 256;
+    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE_BYTES + 8 * 4096 + 512;   // ... a slab per softmax warp
 };
 
 template <int D>
@@ -284,42 +344,27 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     constexpr int TILE_BYTES = Layout<D>::TILE_BYTES;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *ring = smem + 2 * TILE_BYTES;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(ring + STAGES * TILE_BYTES);
-    uint64_t *full = bars, *empty = bars + STAGES, *q_full = bars + 2 * STAGES, *tail = q_full + 1;
-    uint64_t *s_full = tail + 1, *p_ready = s_full + 2, *o_full = p_ready + 4;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(o_full + 2);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *ring = smem + 2 * TILE_BYTES, *slabs = ring + STAGES * TILE_BYTES;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(slabs + 8 * 4096);
+    uint64_t *full = bars, *empty = bars + STAGES, *q_full = bars + 2 * STAGES, *q_empty = q_full + 1, *tail = q_full + 2;
+    uint64_t *s_full = tail + 1, *o_full = s_full + 2, *p_ready = o_full + 2, *o_empty = p_ready + 4;
+    uint64_t *answered = o_empty + 2, *read = answered + 2;
+    uint4 *responses = reinterpret_cast<uint4 *>(read + 2 + ((bars - read) & 1));   // two, 16-byte aligned
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(responses + 2);
+    const int items = gridDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        mbar_init(q_full, 1);
-        mbar_init(tail, 1);
-        for (int u = 0; u < 2; ++u) {
-            mbar_init(&s_full[u], 1);
-            mbar_init(&p_ready[2 * u], 4);       // keys 0-63 of a block, 64-127
-            mbar_init(&p_ready[2 * u + 1], 4);
-            mbar_init(&o_full[u], 1);
+        for (uint64_t *b = bars; b < p_ready; ++b) mbar_init(b, 1);
+        for (uint64_t *b = p_ready; b < answered; ++b) mbar_init(b, 4);   // four warps each
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&answered[i], 1);
+            mbar_init(&read[i], 9);   // the MMA warp and the softmax warps
         }
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    pdl_wait();
-    const int g = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
-    int b, len, item;
-    find_slot(p, sl, gridDim.x / p.kv_heads - 1 - blockIdx.x / p.kv_heads, lane, &b, &len, &item);
-    const int64_t units = (int64_t)((len + TILE - 1) / TILE) * group, u0 = 2 * (int64_t)item;
-    if (u0 >= units) return;   // block-uniform, before tensor memory is allocated
-    const bool two = u0 + 1 < units;
-    const int t0 = (int)(u0 / group), h0 = g * group + (int)(u0 % group);
-    const int t1 = two ? (int)((u0 + 1) / group) : t0, h1 = g * group + (int)((u0 + 1) % group);
-    const int blocks = t1 + 1;
-
     if (warp == 9) {
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
@@ -329,163 +374,204 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     tc_fence_after();
     // all 512 columns are the block's, so they start at 0: S0, S1 (128 each), then O0, O1 (D each)
     constexpr uint32_t tmem = 0;
+    pdl_wait();
 
     if (warp >= 8) {
         regs_down();
         if (warp == 8) {
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * TILE_BYTES);
-                load_tile<D>(smem, &tmQ, q_full, h0 * D, b + t0 * TILE);
-                if (two) load_tile<D>(smem + TILE_BYTES, &tmQ, q_full, h1 * D, b + t1 * TILE);
-            }
             uint32_t stage = 0, phase = 0;
+            int issued = 0, done = 0, tails = 0;   // ring loads, work items, last V tiles
             bool ok = true;
-            int issued = 0;
-            for (int i = 0; i < 2 * blocks && ok; ++i) {   // K(0), V(0), K(1), ...
-                if (!(ok = warp_all(mbar_wait(&empty[stage], phase ^ 1)))) break;
-                const int row = b + (i >> 1) * TILE, rows = len - (i >> 1) * TILE;
-                uint8_t *dst = ring + stage * TILE_BYTES;
-                if ((i & 1) && rows < TILE) {   // the sequence's last V tile
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(tail, TILE_BYTES);
-                        load_tile<D>(dst, &tmV, tail, g * D, row);
-                    }
-                    if (!(ok = warp_all(mbar_wait(tail, 0)))) break;
-                    clear_rows<D>(dst, rows, lane);
-                    if (lane == 0) mbar_arrive(&full[stage]);
-                } else if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[stage], TILE_BYTES);
-                    load_tile<D>(dst, i & 1 ? &tmV : &tmK, &full[stage], g * D, row);
+            int asked = 0;
+            for (int it = blockIdx.x; it >= 0 && ok;) {
+                const Pair w = find_pair(p, sl, it, items, lane);
+                if (w.any && !(ok = warp_all(mbar_wait(q_empty, (done & 1) ^ 1)))) break;
+                done += w.any;
+                if (w.any && lane == 0) {
+                    mbar_arrive_expect_tx(q_full, (w.two ? 2 : 1) * TILE_BYTES);
+                    load_tile<D>(smem, &tmQ, q_full, w.h0 * D, w.b + w.t0 * TILE);
+                    if (w.two) load_tile<D>(smem + TILE_BYTES, &tmQ, q_full, w.h1 * D, w.b + w.t1 * TILE);
                 }
-                ++issued;
-                if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                for (int i = 0; w.any && i < 2 * (w.t1 + 1) && ok; ++i) {   // K(0), V(0), K(1), ...
+                    if (!(ok = warp_all(mbar_wait(&empty[stage], phase ^ 1)))) break;
+                    const int row = w.b + (i >> 1) * TILE, rows = w.len - (i >> 1) * TILE;
+                    uint8_t *dst = ring + stage * TILE_BYTES;
+                    if ((i & 1) && rows < TILE) {   // the sequence's last V tile
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(tail, TILE_BYTES);
+                            load_tile<D>(dst, &tmV, tail, w.g * D, row);
+                        }
+                        if (!(ok = warp_all(mbar_wait(tail, tails++ & 1)))) break;
+                        clear_rows<D>(dst, rows, lane);
+                        if (lane == 0) mbar_arrive(&full[stage]);
+                    } else if (lane == 0) {
+                        mbar_arrive_expect_tx(&full[stage], TILE_BYTES);
+                        load_tile<D>(dst, i & 1 ? &tmV : &tmK, &full[stage], w.g * D, row);
+                    }
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1; }
+                }
+                // asked for only now, with two blocks of this item still to be computed: early enough,
+                // and late enough for the items to go where there is room
+                if (!ok || !(ok = warp_all(mbar_wait(&read[asked & 1], ((asked >> 1) & 1) ^ 1)))) break;
+                if (lane == 0) request_item(&responses[asked & 1], &answered[asked & 1]);
+                it = next_item(responses, answered, nullptr, asked++, lane);
             }
             // every copy lands before the CTA may leave
-            mbar_wait(q_full, 0);
+            if (done) mbar_wait(q_full, (done - 1) & 1);
             for (int s = 0; s < STAGES && s < issued; ++s) mbar_wait(&full[s], ((issued - 1 - s) / STAGES) & 1);
-        } else if (warp == 9 && elect_one()) {
+        } else if (warp == 9) {
             const uint32_t q0 = smem_u32(smem), q1 = q0 + TILE_BYTES, r0 = smem_u32(ring);
             const uint32_t S0 = tmem, S1 = tmem + TILE, O0 = tmem + 2 * TILE, O1 = O0 + D;
-            bool ok = mbar_wait(q_full, 0) && mbar_wait(&full[0], 0);
-            tc_fence_after();
-            if (ok) {
-                mma_cols<D>(S0, q0, r0);
-                tc_commit(&s_full[0]);
-                if (two) {
-                    mma_cols<D>(S1, q1, r0);
-                    tc_commit(&s_full[1]);
-                }
-                tc_commit(&empty[0]);
-            }
-            for (int j = 0; j < blocks && ok; ++j) {
-                const int vi = 2 * j + 1, ki = vi + 1, vs = vi % STAGES, ks = ki % STAGES;
-                const bool more0 = j < t0, more1 = two && j < t1;   // another block after this one
-                if (!(ok = mbar_wait(&full[vs], (vi / STAGES) & 1))) break;
-                if (j <= t0) {
-                    if (!(ok = mbar_wait(&p_ready[0], j & 1))) break;
+            bool ok = true;
+            int done = 0, done1 = 0, load = 0, c0 = 0, c1 = 0;   // items, items with a second unit, ring loads, blocks
+            for (int it = blockIdx.x, n = 0; it >= 0 && ok; it = next_item(responses, answered, read, n++, lane)) {
+                const Pair w = find_pair(p, sl, it, items, lane);
+                if (!w.any) continue;
+                const int t0 = w.t0, t1 = w.t1, blocks = t1 + 1;
+                const bool two = w.two;
+                if (elect_one()) {
+                    ok = mbar_wait(q_full, done & 1) && mbar_wait(&full[load % STAGES], (load / STAGES) & 1);
                     tc_fence_after();
-                    mma_rows<D, 0, 4>(O0, S0, r0 + vs * TILE_BYTES, j > 0);
-                    if (!(ok = mbar_wait(&p_ready[1], j & 1))) break;
-                    tc_fence_after();
-                    mma_rows<D, 4, 8>(O0, S0, r0 + vs * TILE_BYTES, true);
-                    if (!more0) tc_commit(&o_full[0]);
+                    if (ok) {
+                        const uint32_t k = r0 + load % STAGES * TILE_BYTES;
+                        mma_cols<D>(S0, q0, k);
+                        tc_commit(&s_full[0]);
+                        if (two) {
+                            mma_cols<D>(S1, q1, k);
+                            tc_commit(&s_full[1]);
+                        }
+                        tc_commit(&empty[load % STAGES]);
+                        if (blocks == 1) tc_commit(q_empty);
+                    }
+                    for (int j = 0; j < blocks && ok; ++j) {
+                        const int vi = load + 2 * j + 1, ki = vi + 1, vs = vi % STAGES, ks = ki % STAGES;
+                        const bool more0 = j < t0, more1 = two && j < t1;   // another block after this one
+                        if (!(ok = mbar_wait(&full[vs], (vi / STAGES) & 1))) break;
+                        if (j <= t0) {
+                            // the unit's last output has left its accumulator
+                            if (j == 0 && !(ok = mbar_wait(&o_empty[0], (done & 1) ^ 1))) break;
+                            if (!(ok = mbar_wait(&p_ready[0], (c0 + j) & 1))) break;
+                            tc_fence_after();
+                            mma_rows<D, 0, 4>(O0, S0, r0 + vs * TILE_BYTES, j > 0);
+                            if (!(ok = mbar_wait(&p_ready[1], (c0 + j) & 1))) break;
+                            tc_fence_after();
+                            mma_rows<D, 4, 8>(O0, S0, r0 + vs * TILE_BYTES, true);
+                            if (!more0) tc_commit(&o_full[0]);
+                        }
+                        if (more0 || more1) {
+                            if (!(ok = mbar_wait(&full[ks], (ki / STAGES) & 1))) break;
+                            tc_fence_after();
+                        }
+                        if (more0) {
+                            mma_cols<D>(S0, q0, r0 + ks * TILE_BYTES);
+                            tc_commit(&s_full[0]);
+                        }
+                        if (two) {
+                            if (j == 0 && !(ok = mbar_wait(&o_empty[1], (done1 & 1) ^ 1))) break;
+                            if (!(ok = mbar_wait(&p_ready[2], (c1 + j) & 1))) break;
+                            tc_fence_after();
+                            mma_rows<D, 0, 4>(O1, S1, r0 + vs * TILE_BYTES, j > 0);
+                            if (!(ok = mbar_wait(&p_ready[3], (c1 + j) & 1))) break;
+                            tc_fence_after();
+                            mma_rows<D, 4, 8>(O1, S1, r0 + vs * TILE_BYTES, true);
+                            if (!more1) tc_commit(&o_full[1]);
+                        }
+                        tc_commit(&empty[vs]);
+                        if (more1) {
+                            mma_cols<D>(S1, q1, r0 + ks * TILE_BYTES);
+                            tc_commit(&s_full[1]);
+                        }
+                        if (more0 || more1) {
+                            tc_commit(&empty[ks]);
+                            if (j + 2 == blocks) tc_commit(q_empty);   // the last scores are issued
+                        }
+                    }
                 }
-                if (more0 || more1) {
-                    if (!(ok = mbar_wait(&full[ks], (ki / STAGES) & 1))) break;
-                    tc_fence_after();
-                }
-                if (more0) {
-                    mma_cols<D>(S0, q0, r0 + ks * TILE_BYTES);
-                    tc_commit(&s_full[0]);
-                }
-                if (two) {
-                    if (!(ok = mbar_wait(&p_ready[2], j & 1))) break;
-                    tc_fence_after();
-                    mma_rows<D, 0, 4>(O1, S1, r0 + vs * TILE_BYTES, j > 0);
-                    if (!(ok = mbar_wait(&p_ready[3], j & 1))) break;
-                    tc_fence_after();
-                    mma_rows<D, 4, 8>(O1, S1, r0 + vs * TILE_BYTES, true);
-                    if (!more1) tc_commit(&o_full[1]);
-                }
-                tc_commit(&empty[vs]);
-                if (more1) {
-                    mma_cols<D>(S1, q1, r0 + ks * TILE_BYTES);
-                    tc_commit(&s_full[1]);
-                }
-                if (more0 || more1) tc_commit(&empty[ks]);
+                ok = warp_all(ok);
+                ++done;
+                done1 += two;
+                load += 2 * blocks;
+                c0 += t0 + 1;
+                if (two) c1 += t1 + 1;
             }
         }
     } else {
         regs_up();
-        const int u = warp >> 2, row = threadIdx.x & 127, t = u ? t1 : t0;
-        const int last = u && !two ? -1 : t;
+        const int u = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 tensor-memory lanes
         const uint32_t S = tmem + u * TILE + lanes, O = tmem + 2 * TILE + u * D + lanes;
         const float c = p.scale * LOG2E;
-        float m = -INFINITY, l = 0.0f;   // reference of the exponentials (times c), row sum
         bool ok = true;
-        for (int j = 0; j <= last && ok; ++j) {
-            if (!(ok = warp_all(mbar_wait(&s_full[u], j & 1)))) break;
-            tc_fence_after();
-            if (j == t) mask_diagonal(S, row);
-            uint32_t r[128];
-            tmem_ld_row(S, r);
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        int done = 0, seen = 0;   // work items and blocks of this unit
+        for (int it = blockIdx.x, n = 0; it >= 0 && ok; it = next_item(responses, answered, read, n++, lane)) {
+            const Pair w = find_pair(p, sl, it, items, lane);
+            if (!w.any || (u && !w.two)) continue;
+            const int t = u ? w.t1 : w.t0;
+            float m = -INFINITY, l = 0.0f;   // reference of the exponentials (times c), row sum
+            for (int j = 0; j <= t && ok; ++j, ++seen) {
+                if (!(ok = warp_all(mbar_wait(&s_full[u], seen & 1)))) break;
+                tc_fence_after();
+                if (j == t) mask_diagonal(S, row);
+                uint32_t r[128];
+                tmem_ld_row(S, r);
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int e = 0; e < 128; e += 2)
-                mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-            if (j == 0) {
-                m = top;
-            } else {
-                const bool grew = top > m + 8.0f;
-                if (__any_sync(0xffffffffu, grew)) {
-                    const float f = grew ? ex2(m - top) : 1.0f;
-                    if (grew) m = top;
-                    l *= f;
+                for (int e = 0; e < 128; e += 2)
+                    mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                if (j == 0) {
+                    m = top;
+                } else {
+                    const bool grew = top > m + 8.0f;
+                    if (__any_sync(0xffffffffu, grew)) {
+                        const float f = grew ? ex2(m - top) : 1.0f;
+                        if (grew) m = top;
+                        l *= f;
 #pragma unroll 1
-                    for (int i = 0; i < D / 16; ++i) {
-                        uint32_t a[16];
-                        tmem_ld_32x32b_x16(O + 16 * i, a);
-                        tmem_ld_wait();
+                        for (int i = 0; i < D / 16; ++i) {
+                            uint32_t a[16];
+                            tmem_ld_32x32b_x16(O + 16 * i, a);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
-                        tmem_st_32x32b_x16(O + 16 * i, a);
+                            for (int e = 0; e < 16; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
+                            tmem_st_32x32b_x16(O + 16 * i, a);
+                        }
                     }
                 }
-            }
-            const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-m, -m);
-            uint64_t sum[2] = {0, 0};
+                const uint64_t c2 = f2_pack(c, c), m2 = f2_pack(-m, -m);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {   // keys 0-63, 64-127: the first product starts on the first half
-                uint32_t w[32];
+                for (int i = 0; i < 2; ++i) {   // keys 0-63, 64-127: the first product starts on the first half
+                    uint32_t w[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const uint64_t x = f2_fma((uint64_t)r[64 * i + 2 * e + 1] << 32 | r[64 * i + 2 * e], c2, m2);
-                    const uint64_t y = e % EX2_PERIOD < EX2_BY_FMA ? ex2_fma(x) : ex2_pair(x);
-                    sum[e & 1] = f2_add(sum[e & 1], y);
-                    float y0, y1;
-                    f2_unpack(y, y0, y1);
-                    w[e] = pack_bf16x2(y0, y1);
+                    for (int e = 0; e < 32; ++e) {
+                        const uint64_t x = f2_fma((uint64_t)r[64 * i + 2 * e + 1] << 32 | r[64 * i + 2 * e], c2, m2);
+                        const uint64_t y = e % EX2_PERIOD < EX2_BY_FMA ? ex2_fma(x) : ex2_pair(x);
+                        sum[e & 1] = f2_add(sum[e & 1], y);
+                        float y0, y1;
+                        f2_unpack(y, y0, y1);
+                        w[e] = pack_bf16x2(y0, y1);
+                    }
+                    tmem_st_32x32b_x32(S + 32 * i, w);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_ready[2 * u + i]);
                 }
-                tmem_st_32x32b_x32(S + 32 * i, w);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&p_ready[2 * u + i]);
+                float s0, s1;
+                f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
             }
-            float s0, s1;
-            f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
-            l += s0 + s1;
-        }
-        ok = last >= 0 && ok && warp_all(mbar_wait(&o_full[u], 0));
-        if (ok) {
+            if (!ok || !(ok = warp_all(mbar_wait(&o_full[u], done & 1)))) break;
+            ++done;
             tc_fence_after();
-            const int q0 = t * TILE + (warp & 3) * 32, h = u ? h1 : h0;   // the warp's first query
-            // the unit's Q tile is no longer read: its memory passes the output on
-            store_rows<D>(O, 1.0f / l, smem + u * TILE_BYTES + (warp & 3) * 4096,
-                          p.o + (int64_t)(b + q0) * p.ldo + (int64_t)h * D, p.ldo, len - q0, lane);
-            if (q0 + lane < len) p.lse[(int64_t)h * p.M + b + q0 + lane] = fmaf(m, LN2, logf(l));
+            const int q0 = t * TILE + (warp & 3) * 32, h = u ? w.h1 : w.h0;   // the warp's first query
+            store_rows<D>(O, 1.0f / l, slabs + warp * 4096, p.o + (int64_t)(w.b + q0) * p.ldo + (int64_t)h * D, p.ldo,
+                          w.len - q0, lane);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&o_empty[u]);
+            if (q0 + lane < w.len) p.lse[(int64_t)h * p.M + w.b + q0 + lane] = fmaf(m, LN2, logf(l));
         }
         tc_fence_before();
     }
@@ -565,14 +651,10 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         prefetch_tensormap(&tmV);
     }
     pdl_wait();
-    const int g = blockIdx.x % p.kv_heads, group = p.heads / p.kv_heads;
-    int b, len, item;
-    find_slot(p, sl, gridDim.x / p.kv_heads - 1 - blockIdx.x / p.kv_heads, lane, &b, &len, &item);
-    const int64_t units = (int64_t)((len + TILE - 1) / TILE) * group, u0 = 2 * (int64_t)item;
-    if (u0 >= units) return;   // block-uniform, before tensor memory is allocated
-    const bool two = u0 + 1 < units;
-    const int t0 = (int)(u0 / group), h0 = g * group + (int)(u0 % group);
-    const int t1 = two ? (int)((u0 + 1) / group) : t0, h1 = g * group + (int)((u0 + 1) % group);
+    const Pair w = find_pair(p, sl, blockIdx.x, gridDim.x, lane);
+    if (!w.any) return;   // block-uniform, before tensor memory is allocated
+    const int b = w.b, len = w.len, g = w.g, t0 = w.t0, t1 = w.t1, h0 = w.h0, h1 = w.h1;
+    const bool two = w.two;
     const int blocks = t1 + 1;
 
     if (warp == GRAD_WARPS + 1) {
@@ -1166,7 +1248,7 @@ static pact_status map_rows(CUtensorMap *m, const pact_bf16 *base, int64_t cols,
 // len group / 256 + 127 group / 256 + 1/2.
 static Slots pair_slots(const Params &p) {
     const int group = p.heads / p.kv_heads;
-    return {group, 2 * TILE, group / 2 + 2};
+    return {group, 8, group / 2 + 2};   // 256 = two tiles
 }
 
 template <int D>
@@ -1199,7 +1281,7 @@ static pact_status run_bwd(const Params &p, cudaStream_t st) {
     if (s == PACT_OK) s = map_rows(&k, p.k, nk, p.M, p.ldk, what);
     if (s == PACT_OK) s = map_rows(&v, p.v, nk, p.M, p.ldv, what);
     if (s != PACT_OK) return s;
-    const Slots pairs = pair_slots(p), tiles = {1, TILE, 1};
+    const Slots pairs = pair_slots(p), tiles = {1, 7, 1};   // 128
     const int64_t grid_q = pairs.first(p.M, p.nseq) * p.kv_heads, grid_kv = tiles.first(p.M, p.nseq) * p.kv_heads;
     PACT_CHECK(grid_q <= 0x7FFFFFFF && grid_kv <= 0x7FFFFFFF, PACT_ERR_SHAPE, "%s: too many tiles", what);
     s = launch_dep(dq::k_attn_dq<D>, dim3((unsigned)grid_q), dim3(GRAD_THREADS), dq::Layout<D>::SMEM, st, what, q, g,
