@@ -252,7 +252,7 @@ __device__ __forceinline__ void find_slot(const Params &p, const Slots &sl, int6
 // Work item `it` of `items` (slots times key heads), in order of falling slots (a sequence's last and
 // longest tiles first), the key heads of a slot side by side: a pair of units of one key head,
 // query tiles t0, t1 of heads h0, h1 (t1 = t0 where there is no second).
-struct Pair {
+struct __align__(16) Pair {
     int b, len, g, t0, t1, h0, h1;
     bool any, two;
 };
@@ -271,6 +271,20 @@ __device__ __forceinline__ Pair find_pair(const Params &p, const Slots &sl, int 
     w.h0 = w.g * group + hh;
     w.t1 = w.t0 + (w.two && hh + 1 == group);
     w.h1 = w.g * group + (hh + 1 == group ? 0 : hh + 1);
+    return w;
+}
+
+// The n-th pair the TMA warp planned, from two slots of shared memory in turn (a warp); `read` learns that
+// it has been read.  any = false: no more.
+__device__ __forceinline__ Pair planned_pair(const Pair *plan, uint64_t *planned, uint64_t *read, int n, int lane) {
+    Pair w;
+    if (!warp_all(mbar_wait(&planned[n & 1], (n >> 1) & 1))) {
+        w.any = false;
+        return w;
+    }
+    w = plan[n & 1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&read[n & 1]);
     return w;
 }
 
@@ -298,15 +312,6 @@ __device__ __forceinline__ int answered_item(const uint4 *response) {
         : "r"(smem_u32(response))
         : "memory");
     return got ? (int)x : -1;
-}
-// A warp's next item: the n-th answer, from two slots in turn; `read` learns that the warp has read it.
-__device__ __forceinline__ int next_item(const uint4 *responses, uint64_t *answered, uint64_t *read, int n, int lane) {
-    if (!warp_all(mbar_wait(&answered[n & 1], (n >> 1) & 1))) return -1;
-    const int it = answered_item(&responses[n & 1]);
-    fence_proxy_async_smem();   // the next answer is written by the async proxy
-    __syncwarp();
-    if (read && lane == 0) mbar_arrive(&read[n & 1]);
-    return it;
 }
 
 constexpr int SPLIT_THREADS = 384;   // three warpgroups; registers are moved to the first two
@@ -348,18 +353,17 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
     uint64_t *bars = reinterpret_cast<uint64_t *>(slabs + 8 * 4096);
     uint64_t *full = bars, *empty = bars + STAGES, *q_full = bars + 2 * STAGES, *q_empty = q_full + 1, *tail = q_full + 2;
     uint64_t *s_full = tail + 1, *o_full = s_full + 2, *p_ready = o_full + 2, *o_empty = p_ready + 4;
-    uint64_t *answered = o_empty + 2, *read = answered + 2;
-    uint4 *responses = reinterpret_cast<uint4 *>(read + 2 + ((bars - read) & 1));   // two, 16-byte aligned
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(responses + 2);
+    uint64_t *read = o_empty + 2, *planned = read + 2, *answered = planned + 2;
+    Pair *plan = reinterpret_cast<Pair *>(answered + 1 + ((answered + 1 - bars) & 1));   // two; 16-byte aligned
+    uint4 *response = reinterpret_cast<uint4 *>(plan + 2);
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(response + 1);
     const int items = gridDim.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (uint64_t *b = bars; b < p_ready; ++b) mbar_init(b, 1);
-        for (uint64_t *b = p_ready; b < answered; ++b) mbar_init(b, 4);   // four warps each
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&answered[i], 1);
-            mbar_init(&read[i], 9);   // the MMA warp and the softmax warps
-        }
+        for (uint64_t *b = p_ready; b < read; ++b) mbar_init(b, 4);       // four warps each
+        for (uint64_t *b = read; b < planned; ++b) mbar_init(b, 9);       // the MMA warp and the softmax warps
+        for (uint64_t *b = planned; b <= answered; ++b) mbar_init(b, 1);
         fence_barrier_init();
         prefetch_tensormap(&tmQ);
         prefetch_tensormap(&tmK);
@@ -383,16 +387,41 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             int issued = 0, done = 0, tails = 0;   // ring loads, work items, last V tiles
             bool ok = true;
             int asked = 0;
-            for (int it = blockIdx.x; it >= 0 && ok;) {
-                const Pair w = find_pair(p, sl, it, items, lane);
-                if (w.any && !(ok = warp_all(mbar_wait(q_empty, (done & 1) ^ 1)))) break;
-                done += w.any;
-                if (w.any && lane == 0) {
+            auto ask = [&] {
+                if (lane == 0) request_item(response, answered);
+                ++asked;
+            };
+            auto answer = [&] {
+                if (!(ok = warp_all(mbar_wait(answered, (asked - 1) & 1)))) return -1;
+                const int it = answered_item(response);
+                fence_proxy_async_smem();   // the next answer is written by the async proxy
+                __syncwarp();
+                return it;
+            };
+            for (int it = blockIdx.x; ok;) {
+                Pair w;
+                w.any = false;
+                while (it >= 0 && ok && !(w = find_pair(p, sl, it, items, lane)).any) {   // slots without work
+                    ask();
+                    it = answer();
+                }
+                if (!ok || !(ok = warp_all(mbar_wait(&read[done & 1], ((done >> 1) & 1) ^ 1)))) break;
+                if (lane == 0) {
+                    plan[done & 1] = w;
+                    mbar_arrive(&planned[done & 1]);
+                }
+                if (!w.any || !(ok = warp_all(mbar_wait(q_empty, (done & 1) ^ 1)))) break;
+                ++done;
+                if (lane == 0) {
                     mbar_arrive_expect_tx(q_full, (w.two ? 2 : 1) * TILE_BYTES);
                     load_tile<D>(smem, &tmQ, q_full, w.h0 * D, w.b + w.t0 * TILE);
                     if (w.two) load_tile<D>(smem + TILE_BYTES, &tmQ, q_full, w.h1 * D, w.b + w.t1 * TILE);
                 }
-                for (int i = 0; w.any && i < 2 * (w.t1 + 1) && ok; ++i) {   // K(0), V(0), K(1), ...
+                // the next item is asked for two blocks before the last loads: early enough for its plan to
+                // wait for the other warps, late enough for the items to go where there is room
+                const int loads = 2 * (w.t1 + 1), ask_at = max(0, loads - 4);
+                for (int i = 0; i < loads && ok; ++i) {   // K(0), V(0), K(1), ...
+                    if (i == ask_at) ask();
                     if (!(ok = warp_all(mbar_wait(&empty[stage], phase ^ 1)))) break;
                     const int row = w.b + (i >> 1) * TILE, rows = w.len - (i >> 1) * TILE;
                     uint8_t *dst = ring + stage * TILE_BYTES;
@@ -411,13 +440,10 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1; }
                 }
-                // asked for only now, with two blocks of this item still to be computed: early enough,
-                // and late enough for the items to go where there is room
-                if (!ok || !(ok = warp_all(mbar_wait(&read[asked & 1], ((asked >> 1) & 1) ^ 1)))) break;
-                if (lane == 0) request_item(&responses[asked & 1], &answered[asked & 1]);
-                it = next_item(responses, answered, nullptr, asked++, lane);
+                if (ok) it = answer();
             }
-            // every copy lands before the CTA may leave
+            // every copy and answer lands before the CTA may leave
+            if (asked) mbar_wait(answered, (asked - 1) & 1);
             if (done) mbar_wait(q_full, (done - 1) & 1);
             for (int s = 0; s < STAGES && s < issued; ++s) mbar_wait(&full[s], ((issued - 1 - s) / STAGES) & 1);
         } else if (warp == 9) {
@@ -425,9 +451,9 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             const uint32_t S0 = tmem, S1 = tmem + TILE, O0 = tmem + 2 * TILE, O1 = O0 + D;
             bool ok = true;
             int done = 0, done1 = 0, load = 0, c0 = 0, c1 = 0;   // items, items with a second unit, ring loads, blocks
-            for (int it = blockIdx.x, n = 0; it >= 0 && ok; it = next_item(responses, answered, read, n++, lane)) {
-                const Pair w = find_pair(p, sl, it, items, lane);
-                if (!w.any) continue;
+            while (ok) {
+                const Pair w = planned_pair(plan, planned, read, done, lane);
+                if (!w.any) break;
                 const int t0 = w.t0, t1 = w.t1, blocks = t1 + 1;
                 const bool two = w.two;
                 if (elect_one()) {
@@ -504,9 +530,10 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         const float c = p.scale * LOG2E;
         bool ok = true;
         int done = 0, seen = 0;   // work items and blocks of this unit
-        for (int it = blockIdx.x, n = 0; it >= 0 && ok; it = next_item(responses, answered, read, n++, lane)) {
-            const Pair w = find_pair(p, sl, it, items, lane);
-            if (!w.any || (u && !w.two)) continue;
+        for (int n = 0; ok; ++n) {
+            const Pair w = planned_pair(plan, planned, read, n, lane);
+            if (!w.any) break;
+            if (u && !w.two) continue;
             const int t = u ? w.t1 : w.t0;
             float m = -INFINITY, l = 0.0f;   // reference of the exponentials (times c), row sum
             for (int j = 0; j <= t && ok; ++j, ++seen) {
