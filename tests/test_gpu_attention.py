@@ -23,6 +23,9 @@ CASES = [
     ([1023], 0, 12, 2, 128),
     ([513, 511], 0, 32, 8, 64),
     ([3] * 70 + [130], 0, 4, 1, 128),
+    ([200, 0, 1] * 20, 11, 3, 1, 64),
+    ([7, 300, 129, 2] * 8, 0, 2, 2, 128),
+    ([260] + [0] * 40, 0, 5, 5, 64),
     ([1100, 5, 900], 43, 7, 7, 64),
 ]
 IDS = [f"{len(c[0])}seq-{sum(c[0])}+{c[1]}-h{c[2]}k{c[3]}d{c[4]}" for c in CASES]
