@@ -487,7 +487,8 @@ PACT_API pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o,
  *   dq_i = scale sum_j dS_ij k_j;  dk_j = scale sum dS_ij q_i,  dv_j = sum P_ij do_i  over
  *   the rows i and the query heads of j's group.
  * P and dS enter their products as BF16; every sum is FP32 in a fixed order (repeated
- * calls agree bit for bit).  Rows of no sequence are left as they were.  workspace
+ * calls agree bit for bit).  Rows of no sequence are left as they were; outputs must not
+ * overlap the inputs.  workspace
  * (device, 16-byte aligned, >= pact_attention_bwd_workspace_bytes(M, heads)) is scratch;
  * calls that share it must not overlap on the GPU. */
 typedef struct {

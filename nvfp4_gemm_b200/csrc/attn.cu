@@ -72,8 +72,10 @@ __device__ __forceinline__ uint64_t ex2_fma(uint64_t x) {
     const uint32_t lo = (uint32_t)y + ((uint32_t)t << 23), hi = (uint32_t)(y >> 32) + ((uint32_t)(t >> 32) << 23);
     return (uint64_t)hi << 32 | lo;
 }
-// Of EX2_PERIOD pairs, EX2_BY_FMA go to the FP32 units.
-constexpr int EX2_PERIOD = 8, EX2_BY_FMA = 2, EX2_BY_FMA_DQ = 2, EX2_BY_FMA_DKV = 3;
+// Of EX2_PERIOD pairs, this many go to the FP32 units.  Gradients over 4 x 2048 tokens, 24 and 8 heads of 128:
+// 355 us with none, 348 so, 362 with half of dk and dv's.  The forward gains nothing (114 us with
+// none, one or two, 120 with three).
+constexpr int EX2_PERIOD = 8, EX2_BY_FMA_DQ = 2, EX2_BY_FMA_DKV = 1;
 
 // 128 columns of a lane.
 __device__ __forceinline__ void tmem_ld_row(uint32_t taddr, uint32_t (&r)[128]) {
@@ -174,9 +176,8 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int row, int lane) {
     __syncwarp();
 }
 
-// N accumulator columns (from `taddr`) of a warp's 32 lanes, each times its lane's f, as BF16 to rows
-// row0 + lane of dst (leading dimension ld, first column already added), rows from `rows` on left
-// out.  A lane holds a row, so the values pass through 4 KiB of shared memory (16-byte chunk
+// N accumulator columns (from `taddr`) of a warp's 32 lanes, each times its lane's f, as BF16 to the rows of
+// dst (leading dimension ld, first column already added), rows from `rows` on left out.  A lane holds a row, so the values pass through 4 KiB of shared memory (16-byte chunk
 // c of row r at c ^ (r % 8)): stores of whole 128-byte lines, four rows an instruction.
 // Stored straight from the lanes, 32 rows an instruction, a tile took 4.4 us; this way 1.
 template <int N>
@@ -368,20 +369,24 @@ __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.
 static_assert(2 * 128 * 216 + 128 * 72 <= SPLIT_THREADS * 168, "more registers than the block is launched with");
 
 // ------------------------------------------------------------------------- forward
-// A CTA computes two units that share a key head: a unit is a 128-query tile of one query
-// head, and the units of a sequence run tile-major over the group's heads, so a pair is
-// two heads of one tile, or the last head of a tile and the first of the next (one head
-// per group: two tiles).  K and V tiles are loaded once for both.  Two tiles in flight let the
-// tensor core run one unit's products while the other's softmax runs:
+// A CTA computes pairs of units that share a key head; K and V tiles are loaded once for both, and the
+// tensor core runs one unit's products while the other's softmax runs:
 //   warps 0-3, 4-7   softmax of unit 0, 1: a thread owns a query row (a tensor-memory lane),
 //                    so maximum and sum need no exchange.  P overwrites the scores as BF16 and
-//                    is the next product's operand from tensor memory.
-//   warp 8           TMA: the two Q tiles, then K and V tiles through a ring
+//                    is the next product's operand from tensor memory; the product starts on
+//                    its first 64 keys while the rest is computed.
+//   warp 8           the plan, and TMA: the two Q tiles, then K and V tiles through a ring
 //   warp 9           the MMAs, in the order  P0 V(j), S0(j+1), P1 V(j), S1(j+1)
 // The accumulator is rescaled only when a row's maximum grew by more than 2^8 since the
 // last time (any factor cancels in O / l; FP32 has the room), which is rare after the
 // first block.  S(j+1) is issued behind P V(j), so a unit that sees its scores ready
-// also knows its accumulator at rest.
+// also knows its accumulator at rest.  The CTA is persistent: the next pair's Q, K and scores
+// come under the last pair's output.
+// Rounding: P to BF16, as the MMA takes it (by at most 2^-8 of a probability); the row sums add the FP32 values.
+// 4 x 2048 tokens, 24 and 8 heads of 128: 121 us, 849 TFLOP/s of the 103 GFLOP under the diagonal (51% of
+// the measured BF16 rate).  A block of a pair takes 3000 cycles for 2048 of MMAs: a unit's softmax takes
+// 1500 (1024 of them the special-function units'), and with two units in tensor memory it is not
+// wholly under the other's products.
 namespace fwd {
 constexpr int STAGES = 4;
 template <int D>
@@ -622,7 +627,7 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const uint64_t x = f2_fma((uint64_t)r[64 * i + 2 * e + 1] << 32 | r[64 * i + 2 * e], c2, m2);
-                        const uint64_t y = e % EX2_PERIOD < EX2_BY_FMA ? ex2_fma(x) : ex2_pair(x);
+                        const uint64_t y = ex2_pair(x);
                         sum[e & 1] = f2_add(sum[e & 1], y);
                         float y0, y1;
                         f2_unpack(y, y0, y1);
@@ -669,6 +674,11 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // instead of 5): summing dq over key tiles from one kernel takes atomics in FP32, whose
 // order would change the result from call to call, and a pass to clear and round it.
 // This kernel also leaves delta and lse log2(e) for the other one.
+// Rounding: dS to BF16, as the MMA takes it; P, dP and the sums stay FP32.
+// 4 x 2048 tokens, 24 and 8 heads of 128: some 185 us (three products: 37% of the measured BF16 rate).  A
+// block of a pair takes 4700 cycles for 3072 of MMAs; the tensor core waits for dS, 1400 cycles after dP.
+// Tried without gain: persistent CTAs (V's memory is needed to pass the output on), MMA waits
+// moved ahead, dO for delta from its tile.
 // The gradient kernels' softmax needs no exchange between the columns of a row (lse is known), so
 // four warpgroups do it: four warps a scheduler hide one another's latencies, where two left
 // the schedulers idle two cycles in three.
@@ -959,7 +969,11 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 // serve as both operands of their two products from one copy in shared memory.
 // 512 columns: S^T | dP^T | dV | dK; P^T and dS^T lie over S^T and dP^T.  Order of the MMAs:
 //   dV(n) S(n+1) | dK(n) dP(n+1): the exponentials of n+1 run under the second pair.
-// Four warpgroups share the columns: warps 4 w .. 4 w + 3 take queries 32 w .. 32 w + 31 of a tile.
+// Four warpgroups share the columns: warps 4 w .. 4 w + 3 take queries 16 w .. 16 w + 15 of both halves of a tile.
+// Rounding: P and dS to BF16, as the MMA takes them.
+// 4 x 2048 tokens, 24 and 8 heads of 128: some 175 us (four products: 49% of the measured BF16 rate).  A
+// unit takes 2700 cycles for 2048 of MMAs: P (1150) and dV, S(n+1) behind it follow one another,
+// as D = 128 leaves no tensor memory for a second S.
 namespace dkv {
 template <int D>
 struct Layout {

@@ -14,8 +14,10 @@
 // below 3e-4 of the strongest).
 //
 // A matrix that fits the shared memory of a cluster of CTAs takes one kernel and one pass over
-// memory (k_muon_fused): u stays in shared memory between its Gram matrix and P u.  Larger
-// ones take three:
+// memory (k_muon_fused): u stays in shared memory between its Gram matrix and P u.  Its phases
+// (load, Gram matrix, P, P u, store) follow one another in a CTA and overlap only between the two
+// CTAs of an SM: the 392 adapter matrices of 28 layers (rank 16, 406 MB) take 126 us, 3.2 TB/s or
+// 49% of the measured copy rate, the 14 of one layer 18.  Larger ones take three kernels:
 //   k_muon_gram   a slab of the long side per CTA: m' is written, the slab's part of
 //                 u u^T goes to scratch
 //   k_muon_poly   one CTA per matrix: S0 from the parts in a fixed order, then P
