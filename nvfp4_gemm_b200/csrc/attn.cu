@@ -676,7 +676,7 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // This kernel also leaves delta and lse log2(e) for the other one.
 // Rounding: dS to BF16, as the MMA takes it; P, dP and the sums stay FP32.
 // 4 x 2048 tokens, 24 and 8 heads of 128: some 185 us (three products: 37% of the measured BF16 rate).  A
-// block of a pair takes 4700 cycles for 3072 of MMAs; the tensor core waits for dS, 1400 cycles after dP.
+// block of a pair takes 4700 cycles for 48 MMAs of 64; the tensor core waits for dS, 1400 cycles after dP.
 // Tried without gain: persistent CTAs (V's memory is needed to pass the output on), MMA waits
 // moved ahead, dO for delta from its tile.
 // The gradient kernels' softmax needs no exchange between the columns of a row (lse is known), so
@@ -972,8 +972,9 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 // Four warpgroups share the columns: warps 4 w .. 4 w + 3 take queries 16 w .. 16 w + 15 of both halves of a tile.
 // Rounding: P and dS to BF16, as the MMA takes them.
 // 4 x 2048 tokens, 24 and 8 heads of 128: some 175 us (four products: 49% of the measured BF16 rate).  A
-// unit takes 2700 cycles for 2048 of MMAs: P (1150) and dV, S(n+1) behind it follow one another,
-// as D = 128 leaves no tensor memory for a second S.
+// unit takes 2530 cycles for 2048 of MMAs: P (1220, of them 900 the special-function units') and dV, S(n+1)
+// behind it follow one another, as D = 128 leaves no tensor memory for a second S.  A second S at D = 64
+// and a third Q slot changed nothing (P and dS then follow one another without a gap, in the same time).
 namespace dkv {
 template <int D>
 struct Layout {
