@@ -662,6 +662,19 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
     return t
 
 
+def _scratch(ws: Optional[torch.Tensor], need, device, dev: int, stream) -> torch.Tensor:
+    """The caller's workspace (the library checks its size and alignment), or need() bytes of the call's own."""
+    if ws is None:
+        return _new(need(), torch.uint8, device, stream)
+    if not ws.is_cuda:
+        raise TypeError("workspace: expected a CUDA tensor")
+    if ws.get_device() != dev:
+        raise ValueError(f"workspace: on {ws.device}, but the current device is cuda:{dev}")
+    if not ws.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor")
+    return ws
+
+
 def pact_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: Sequence[float], heads: int,
               y: Optional[torch.Tensor] = None, inverse: bool = False, stream=None) -> torch.Tensor:
     """Rotate `heads` heads side by side in x [M x heads * head_dim] (row stride free, e.g. the q|k columns of
@@ -746,9 +759,7 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                          do.data_ptr(), _matrix(do, "do", dev, q.shape), dq.data_ptr(),
                          _matrix(dq, "dq", dev, q.shape), dk.data_ptr(), _matrix(dk, "dk", dev, k.shape),
                          dv.data_ptr(), _matrix(dv, "dv", dev, v.shape))
-    ws = workspace
-    if ws is None:
-        ws = _new(pact_attention_bwd_workspace_bytes(a.M, heads), torch.uint8, q.device, stream)
+    ws = _scratch(workspace, lambda: pact_attention_bwd_workspace_bytes(a.M, heads), q.device, dev, stream)
     _check(_lib.pact_attention_bwd(ctypes.byref(a), ctypes.byref(g), ws.data_ptr(), ws.numel() * ws.element_size(),
                                    _stream(stream)))
     return dq, dk, dv
@@ -793,9 +804,8 @@ def pact_muon_step(weights: Sequence[torch.Tensor], grads: Sequence[torch.Tensor
     weights_out / momenta_out are given; weights_bf16 receive the BF16 copies."""
     mats, fp32 = _muon_matrices(weights, grads, momenta, weights_out if weights_out is not None else weights,
                                 momenta_out if momenta_out is not None else momenta, weights_bf16)
-    ws = workspace
-    if ws is None:
-        ws = _new(int(_lib.pact_muon_workspace_bytes(mats, len(mats))), torch.uint8, weights[0].device, stream)
+    ws = _scratch(workspace, lambda: int(_lib.pact_muon_workspace_bytes(mats, len(mats))), weights[0].device,
+                  weights[0].get_device(), stream)
     _check(_lib.pact_muon_step(mats, len(mats), int(fp32), float(lr), float(momentum), float(weight_decay),
                                int(bool(nesterov)), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
 

@@ -149,3 +149,18 @@ def test_update_needs_a_trainable_layer(monkeypatch):
             L.bind(*args, **kw)
     L.bind(d_out=2, h=1)
     assert L.inputs == (1, L.attn, 2, L.d_qkv)
+
+
+def test_workspaces_off_the_device_are_refused():
+    import nvfp4_gemm_b200 as P
+    x = torch.zeros((4, 128), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    o, lse = P.pact_attention_fwd(x, x, x, cu, 2, 2)
+    w = [torch.zeros((4, 8), device="cuda")]
+    big = torch.zeros((1 << 16, 2), dtype=torch.uint8)
+    for ws, error in ((big, TypeError), (big.cuda()[:, 0], ValueError)):
+        with pytest.raises(error):
+            P.pact_attention_bwd(x, x, x, x, o, lse, cu, 2, 2, workspace=ws)
+        with pytest.raises(error):
+            P.pact_muon_step(w, w, w, lr=0.1, weights_out=[w[0].clone()], momenta_out=[w[0].clone()], workspace=ws)
+    assert not w[0].any()
