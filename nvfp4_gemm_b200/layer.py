@@ -92,6 +92,15 @@ def positions(seq_start: torch.Tensor, M: int) -> torch.Tensor:
     return torch.where((rows >= cu[0]) & (rows < cu[-1]), rows - cu[at], -1).int()
 
 
+def check_packing(seq_start: torch.Tensor, sequences: int, M: int):
+    """seq_start bounds `sequences` packed sequences of M rows."""
+    if seq_start.dim() != 1 or seq_start.numel() != sequences + 1 or sequences < 1:
+        raise ValueError(f"seq_start: shape {list(seq_start.shape)}, expected [{max(sequences, 1) + 1}]")
+    at = seq_start.tolist()
+    if at != sorted(at) or at[0] < 0 or at[-1] > M:
+        raise ValueError(f"seq_start: expected non-decreasing row numbers in [0, {M}]")
+
+
 class PactLayer:
     """Weights are BF16 device tensors in PyTorch [out, in] layout:
     w = {q, k, v, o, gate, up, down}; lora_a = {p: [r, in]}, lora_b = {p: [out, r]};
@@ -223,8 +232,10 @@ class PactLayer:
 
     def pack(self, seq_start: torch.Tensor):
         """Take a batch packed another way: as many row numbers as before (empty sequences
-        fill up).  The layer's buffers are updated in place, on the current stream, so a
-        captured step follows; the op lists' FLOP counts are those of the last pack()."""
+        fill up), none before the one ahead of it.  The layer's buffers are updated in place, on
+        the current stream, so a captured step follows; the op lists' FLOP counts are those of
+        the last pack()."""
+        check_packing(seq_start, self.seq_start.numel() - 1, self.s.M)
         self.seq_start.copy_(seq_start)
         self.pos.copy_(positions(self.seq_start, self.s.M))
         for t in (self.attn, self.lse, self.d_qkv):

@@ -102,3 +102,15 @@ def test_binding_refuses_host_tensors(P):
         P.pact_muon_step([torch.zeros(4, 8)], [torch.zeros(4, 8)], [torch.zeros(4, 8)], lr=0.1)
     with pytest.raises(ValueError):
         P.pact_muon_step([], [], [], lr=0.1)
+
+
+def test_packings_that_are_none_are_refused(P):
+    from nvfp4_gemm_b200.layer import check_packing
+    for good in ([0, 3, 3, 10], [2, 2, 2, 2], [0, 1, 2, 9]):
+        check_packing(torch.tensor(good, dtype=torch.int32), 3, 10)
+    for bad in ([0], [0, 3, 10], [0, 3, 2, 10], [0, 3, 3, 11], [-1, 3, 3, 10]):
+        with pytest.raises(ValueError):
+            check_packing(torch.tensor(bad, dtype=torch.int32), 3, 10)
+    for bad in (torch.tensor(0), torch.zeros((2, 2)), torch.zeros(1)):
+        with pytest.raises(ValueError):
+            check_packing(bad, bad.numel() - 1, 10)
