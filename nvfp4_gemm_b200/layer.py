@@ -220,6 +220,10 @@ class PactLayer:
         if S.H % core.head_dim or S.KV % core.head_dim:
             raise ValueError(f"H = {S.H} and KV = {S.KV} must be multiples of head_dim = {core.head_dim}")
         self.heads, self.kv_heads = S.H // core.head_dim, S.KV // core.head_dim
+        if self.heads % self.kv_heads:
+            raise ValueError(f"{self.heads} query heads do not divide into {self.kv_heads} key heads")
+        # host values, once: a device tensor's would be copied back by every call, and by none in a capture
+        self.inv_freq = torch.as_tensor(core.inv_freq, dtype=torch.float64).cpu().contiguous()
         self.seq_start = core.seq_start.to(device=dev, dtype=torch.int32).clone()
         self.pos = torch.empty(S.M, dtype=torch.int32, device=dev)
         # padding rows are never written: they hold zeros, so what follows stays finite
@@ -298,11 +302,11 @@ class PactLayer:
     def _attention_fwd_ops(self) -> List[Op]:
         if self.attention is None:
             return []
-        S, a, M = self.s, self.attention, self.s.M
+        S, M = self.s, self.s.M
         q, k, v = self.qkv[:, :S.H], self.qkv[:, S.H:S.H + S.KV], self.qkv[:, S.H + S.KV:]
         qk, n = self.qkv[:, :S.H + S.KV], self.heads + self.kv_heads
         return [
-            Op("rope", lambda: P.pact_rope(qk, self.pos, a.inv_freq, n, y=qk), bytes=4 * M * (S.H + S.KV) + 4 * M),
+            Op("rope", lambda: P.pact_rope(qk, self.pos, self.inv_freq, n, y=qk), bytes=4 * M * (S.H + S.KV) + 4 * M),
             Op("attention_fwd", lambda: P.pact_attention_fwd(q, k, v, self.seq_start, self.heads, self.kv_heads,
                                                              o=self.attn, lse=self.lse),
                "attention", 2 * self.attention_flops, bytes=2 * M * (2 * S.H + 2 * S.KV) + 4 * M * self.heads),
@@ -311,7 +315,7 @@ class PactLayer:
     def _attention_bwd_ops(self) -> List[Op]:
         if self.attention is None:
             return []
-        S, a, M = self.s, self.attention, self.s.M
+        S, M = self.s, self.s.M
         q, k, v = self.qkv[:, :S.H], self.qkv[:, S.H:S.H + S.KV], self.qkv[:, S.H + S.KV:]
         d = self.d_qkv
         dqk, n = d[:, :S.H + S.KV], self.heads + self.kv_heads
@@ -321,7 +325,7 @@ class PactLayer:
                 dk=d[:, S.H:S.H + S.KV], dv=d[:, S.H + S.KV:], workspace=self.ws_attn),
                "attention", 5 * self.attention_flops, kernels=2,
                bytes=2 * M * (4 * S.H + 4 * S.KV) + 4 * M * self.heads),
-            Op("rope_bwd", lambda: P.pact_rope(dqk, self.pos, a.inv_freq, n, y=dqk, inverse=True),
+            Op("rope_bwd", lambda: P.pact_rope(dqk, self.pos, self.inv_freq, n, y=dqk, inverse=True),
                bytes=4 * M * (S.H + S.KV) + 4 * M),
         ]
 

@@ -164,3 +164,25 @@ def test_workspaces_off_the_device_are_refused():
         with pytest.raises(error):
             P.pact_muon_step(w, w, w, lr=0.1, weights_out=[w[0].clone()], momenta_out=[w[0].clone()], workspace=ws)
     assert not w[0].any()
+
+
+def test_angles_on_the_device_are_captured_too(monkeypatch):
+    """inv_freq as a device tensor: read once, so that a captured step needs no copy of it."""
+    from nvfp4_gemm_b200.layer import AttentionCore
+    want, inp, freq = build(monkeypatch)
+    monkeypatch.setattr("nvfp4_gemm_b200.layer.AttentionCore", lambda D, starts, f: AttentionCore(
+        D, starts, torch.tensor(f, dtype=torch.float64, device="cuda")))
+    got, _, _ = build(monkeypatch)
+    for L in (want, got):
+        L.bind(dev(inp["h"]), dev(inp["d_out"]))
+        L.step()
+    torch.cuda.synchronize()
+    for t in (got.qkv, got.out, got.dh):
+        t.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got.step()
+    graph.replay()
+    torch.cuda.synchronize()
+    for name in ("qkv", "out", "dh"):
+        assert torch.equal(getattr(got, name), getattr(want, name)), name
