@@ -1,0 +1,35 @@
+// overlap.cuh -- host checks that the outputs of a call share no memory with what else it
+// reads or writes.
+#pragma once
+#include <algorithm>
+#include <cstdint>
+#include <memory>
+#include <new>
+
+#include "common.cuh"
+
+namespace pact {
+
+struct Rows {   // a matrix of `rows` rows of the call, in BF16
+    const pact_bf16 *p;
+    int64_t ld, cols;
+};
+
+// Whether the later matrix's first row lies in the earlier one's rows: the answer for matrices of one row
+// stride (columns of one buffer may lie side by side), and a lower bound of it for others.
+inline bool overlap(Rows a, Rows b, int64_t rows) {
+    if ((uintptr_t)a.p > (uintptr_t)b.p) std::swap(a, b);
+    const int64_t d = (int64_t)(((uintptr_t)b.p - (uintptr_t)a.p) / sizeof(pact_bf16));
+    if (d >= (rows - 1) * a.ld + a.cols) return false;
+    return d % a.ld < a.cols || (d % a.ld + b.cols > a.ld && d / a.ld + 1 < rows);
+}
+
+// Whether any of the first `outs` of `n` matrices overlaps another one of the n.
+inline bool overlap_any(const Rows *m, int outs, int n, int64_t rows) {
+    for (int i = 0; i < outs; ++i)
+        for (int j = i + 1; j < n; ++j)
+            if (overlap(m[i], m[j], rows)) return true;
+    return false;
+}
+
+}  // namespace pact

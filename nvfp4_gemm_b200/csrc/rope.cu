@@ -9,6 +9,7 @@
 // streams heads past them.  8192 rows, 32 heads of 128: 26.2 us with a cold L2, 134 MB at
 // 5.1 TB/s (78% of the measured copy rate); 31.8 us with the angles read from shared memory
 // for every head.
+#include "overlap.cuh"
 #include "quant.cuh"
 
 namespace pact {
@@ -108,6 +109,8 @@ extern "C" pact_status pact_rope(const pact_bf16 *x, int64_t ldx, int64_t M, int
     PACT_CHECK(ldx >= cols && ldy >= cols, PACT_ERR_SHAPE, "pact_rope: leading dimensions below heads * head_dim");
     PACT_CHECK(aligned16(x) && aligned16(y) && ldx % 8 == 0 && ldy % 8 == 0 && ((uintptr_t)positions & 3) == 0,
                PACT_ERR_ALIGN, "pact_rope: 16-byte aligned rows and 4-byte aligned positions needed");
+    PACT_CHECK((x == y && (ldx == ldy || M == 1)) || !overlap({x, ldx, cols}, {y, ldy, cols}, M), PACT_ERR_INVALID_ARG,
+               "pact_rope: y overlaps x but is not x itself with its stride");
     rope::Turns turns = {};
     for (int i = 0; i < head_dim / 2; ++i) turns.per_pos[i] = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
     const rope::Params p = {x, y, positions, ldx, ldy, M, heads, head_dim / 2, inverse != 0};

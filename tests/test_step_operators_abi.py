@@ -114,3 +114,27 @@ def test_packings_that_are_none_are_refused(P):
     for bad in (torch.tensor(0), torch.zeros((2, 2)), torch.zeros(1)):
         with pytest.raises(ValueError):
             check_packing(bad, bad.numel() - 1, 10)
+
+
+def test_overlapping_outputs_are_refused(P):
+    """Matrices of one buffer may lie side by side (nothing below is refused for that alone: the last
+    checks before the overlap are those of alignment, all of which pass)."""
+    lib = P.pact.lib
+    freq, base = (ctypes.c_double * 64)(), 0x100000
+    rope = lambda y, ldy=1024: lib.pact_rope(base, 1024, 4, 4, 128, 0x2000, freq, 0, y, ldy, None)
+    for y, ldy in ((base + 2 * 1024, 1024), (base + 2 * 504, 1024), (base - 2 * 8, 1024), (base, 512),
+                   (base + 2 * 1024, 2048), (base + 2 * 528, 1024)):
+        assert rope(y, ldy) == INVALID and "overlaps" in P.pact_last_error()
+    # M = 300 rows of q (512 columns), k and v (128 each) in one buffer of rows of 768
+    q, k, v = base, base + 2 * 512, base + 2 * 640
+    a = lambda: attention(P, q=q, k=k, v=v, ldq=768, ldk=768, ldv=768)
+    far = 0x800000
+    for o, ldo in ((q, 768), (k, 768), (q + 2 * 768 * 299, 512), (v - 2 * 512, 768), (base - 2 * 8, 512)):
+        assert lib.pact_attention_fwd(a(), o, ldo, 0x6000, None) == INVALID and "overlaps" in P.pact_last_error()
+    names = [f[0] for f in P.pact.c_attention_grad._fields_]
+    good = (far, 512, 0x6000, 2 * far, 512, 3 * far, 768, 3 * far + 1024, 768, 3 * far + 1280, 768)
+    for at in (dict(dq=far), dict(dk=2 * far + 2 * 512), dict(dv=3 * far + 1024), dict(dq=q), dict(dv=v), dict(dk=3 * far + 1008),
+               dict(dv=3 * far + 2 * 768 - 2 * 120)):
+        g = P.pact.c_attention_grad(*[at.get(k, v) for k, v in zip(names, good)])
+        assert lib.pact_attention_bwd(a(), ctypes.byref(g), 0xB000, 1 << 30, None) == INVALID
+        assert "overlap" in P.pact_last_error(), at
