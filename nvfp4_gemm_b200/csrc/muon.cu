@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "overlap.cuh"
 #include "quant.cuh"
 
 namespace pact {
@@ -631,6 +632,15 @@ pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32,
     PACT_CHECK(workspace && ws_bytes >= pact_muon_workspace_bytes(mats, n), PACT_ERR_INVALID_ARG,
                "%s: workspace too small", what);
     PACT_CHECK(aligned16(workspace), PACT_ERR_ALIGN, "%s: workspace must be 16-byte aligned", what);
+    // a matrix given twice would be updated by two CTAs at once
+    Ranges written(3 * (int64_t)n);
+    for (int i = 0; i < n; ++i) {
+        const int64_t size = mats[i].count * mats[i].rows * mats[i].cols;
+        written.add(mats[i].momentum_out, 4 * size);
+        written.add(mats[i].weight_out, 4 * size);
+        written.add(mats[i].weight_bf16, 2 * size);
+    }
+    PACT_CHECK(written.disjoint(), PACT_ERR_INVALID_ARG, "%s: outputs overlap (a matrix given twice?)", what);
     int rmax = 1;
     for (int i = 0; i < n; ++i) rmax = std::max(rmax, (int)std::min(mats[i].rows, mats[i].cols));
     const int nb = blocks_of(rmax);

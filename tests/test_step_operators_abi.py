@@ -138,3 +138,19 @@ def test_overlapping_outputs_are_refused(P):
         g = P.pact.c_attention_grad(*[at.get(k, v) for k, v in zip(names, good)])
         assert lib.pact_attention_bwd(a(), ctypes.byref(g), 0xB000, 1 << 30, None) == INVALID
         assert "overlap" in P.pact_last_error(), at
+
+
+def test_a_matrix_given_twice_is_refused(P):
+    lib, c = P.pact.lib, P.pact.c_muon_matrix
+
+    def call(*at):
+        m = (c * len(at))(*[c(*a, 1, 16, 300) for a in at])
+        return lib.pact_muon_step(m, len(at), 0, 0.1, 0.9, 0.0, 1, 0x10, lib.pact_muon_workspace_bytes(m, len(at)), None)
+    size = 16 * 300 * 4
+    one = [0x1000, 0x100000, 0x100000, 0x200000, 0x200000, 0x300000]
+    for k in (2, 4, 5):   # the same momentum, weight or BF16 copy, and one that begins inside it
+        for shift in (0, size // 2 - 4):
+            other = [0x1000] + [p + size for p in one[1:]]
+            other[k] = one[k] + shift
+            assert call(one, other) == call(other, one) == INVALID and "twice" in P.pact_last_error()
+    assert call([0x1000, 0x100000, 0x100000, 0x200000, 0x100000, None]) == INVALID
