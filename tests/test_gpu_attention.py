@@ -250,3 +250,32 @@ def test_offsets_past_32_bits():
     for name, t in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
         ref64.within(t[M - n:], ref[name], name)
     status_ok()
+
+
+@pytest.mark.parametrize("hq,hk,D", [(4, 2, 64), (3, 1, 128)])
+def test_many_sequences_between_padding(hq, hk, D):
+    """Over 32 sequences, with rows of none ahead of the first and behind the last: as the same sequences
+    without them, and those rows left as they were."""
+    import nvfp4_gemm_b200 as P
+    lens, ahead, behind = [5, 0, 131, 64] * 10, 333, 77
+    q, k, v, cu, starts, M = problem(lens, 0, hq, hk, D)
+    do = bf(5, M, hq * D)
+    o, lse = P.pact_attention_fwd(q, k, v, cu, hq, hk)
+    want = (o, *P.pact_attention_bwd(do, q, k, v, o, lse, cu, hq, hk))
+    rows = slice(ahead, ahead + M)
+
+    def wide(t):
+        out = torch.full((ahead + M + behind, t.shape[1]), math.nan, dtype=t.dtype, device="cuda")
+        out[rows] = t
+        return out
+    q2, k2, v2, do2 = wide(q), wide(k), wide(v), wide(do)
+    outs = [torch.full_like(t, -7.0) for t in (q2, q2, k2, v2)]
+    lse2 = torch.full((hq, ahead + M + behind), -7.0, device="cuda")
+    P.pact_attention_fwd(q2, k2, v2, cu + ahead, hq, hk, o=outs[0], lse=lse2)
+    P.pact_attention_bwd(do2, q2, k2, v2, outs[0], lse2, cu + ahead, hq, hk, dq=outs[1], dk=outs[2], dv=outs[3])
+    status_ok()
+    assert torch.equal(lse2[:, rows], lse)
+    for got, ref in zip(outs, want):
+        assert torch.equal(got[rows], ref)
+        assert bool((got[:ahead] == -7.0).all() and (got[ahead + M:] == -7.0).all())
+    assert bool((lse2[:, :ahead] == -7.0).all() and (lse2[:, ahead + M:] == -7.0).all())

@@ -102,3 +102,40 @@ def test_repeats_captures_and_streams():
     torch.cuda.synchronize()
     for i in (1, 2, 3):
         assert all(torch.equal(x, y) for x, y in zip(outs[i] + mo[i], outs[0] + mo[0]))
+
+
+def test_clusters_and_slabs_in_one_call():
+    """Matrices that fit a cluster, alone and in batches, between ones that take the slabs of scratch, of
+    more than one launch each."""
+    shapes = [(16, 700), (2, 3, 70001), (300, 9), (3, 16, 520), (12, 60000), (1, 1)] * 22
+    w = [rnd(i, *s, std=0.02) for i, s in enumerate(shapes)]
+    g, m = [rnd(500 + i, *s, std=1e-3) for i, s in enumerate(shapes)], [rnd(900 + i, *s) for i, s in enumerate(shapes)]
+    flat = lambda ts: [t for x in ts for t in (x if x.dim() == 3 else [x])]
+    refs = [ref64.muon(a, b, c, 0.02, 0.95, 0.01) for a, b, c in zip(flat(w), flat(g), flat(m))]
+    import nvfp4_gemm_b200 as P
+    P.pact_muon_step(w, g, m, lr=0.02, weight_decay=0.01)
+    torch.cuda.synchronize()
+    for a, c, (rm, rw) in zip(flat(w), flat(m), refs):
+        ref64.within(c, rm, f"m {tuple(a.shape)}")
+        ref64.within(a, rw, f"W {tuple(a.shape)}")
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_gradients_that_are_not_finite_stay_with_their_matrix(bad):
+    """The other matrices of the call, of the same batch and cluster too, are updated as without them."""
+    import nvfp4_gemm_b200 as P
+    w, g = [rnd(1, 6, 16, 200), rnd(2, 40, 16)], [rnd(3, 6, 16, 200), rnd(4, 40, 16)]
+    runs = []
+    for spoil in (False, True):
+        w1, g1 = [t.clone() for t in w], [t.clone() for t in g]
+        m1 = [torch.zeros_like(t) for t in w]
+        if spoil:
+            g1[0][2, 3, 7] = bad
+        P.pact_muon_step(w1, g1, m1, lr=0.1)
+        runs.append((w1, m1))
+    torch.cuda.synchronize()
+    (wa, ma), (wb, mb) = runs
+    keep = [0, 1, 3, 4, 5]
+    assert torch.equal(wa[0][keep], wb[0][keep]) and torch.equal(ma[0][keep], mb[0][keep])
+    assert torch.equal(wa[1], wb[1]) and torch.equal(ma[1], mb[1])
+    assert bool(wb[0][2].isnan().all())

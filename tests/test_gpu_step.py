@@ -186,3 +186,27 @@ def test_angles_on_the_device_are_captured_too(monkeypatch):
     torch.cuda.synchronize()
     for name in ("qkv", "out", "dh"):
         assert torch.equal(getattr(got, name), getattr(want, name)), name
+
+
+def test_an_updated_layer_is_the_layer_of_the_new_adapters(monkeypatch):
+    """Nothing a layer keeps goes back to the adapters it was built with."""
+    from nvfp4_gemm_b200.layer import PactLayer
+    L, inp, _ = build(monkeypatch, trainable=True)
+    L.bind(dev(inp["h"]), dev(inp["d_out"]))
+    L.step()
+    L.update(lr=0.5)
+    before = L.out.clone()
+    L.step()
+    a_q, a_k, a_v, b_q, b_k, b_v, a_o, b_o, a_g, a_u, b_g, b_u, a_d, b_d = [t.clone() for t in L._matrices(L.adapters)]
+    fresh = PactLayer(L.s, {k: dev(v) for k, v in inp["w"].items()},
+                      {"q": a_q, "k": a_k, "v": a_v, "o": a_o, "gate": a_g, "up": a_u, "down": a_d},
+                      {"q": b_q, "k": b_k, "v": b_v, "o": b_o, "gate": b_g, "up": b_u, "down": b_d},
+                      dev(inp["gamma1"]), dev(inp["gamma2"]), attention=L.attention)
+    fresh.bind(dev(inp["h"]), dev(inp["d_out"]))
+    fresh.step()
+    torch.cuda.synchronize()
+    assert not torch.equal(before, L.out)
+    for name in ("out", "dh", "d_qkv"):
+        assert torch.equal(getattr(L, name), getattr(fresh, name)), name
+    for k in L.grads:
+        assert torch.equal(L.grads[k], fresh.grads[k]), k
