@@ -737,6 +737,9 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         prefetch_tensormap(&tmV);
     }
     pdl_wait();
+    // The next kernel may take up its CTAs as this one's leave: what it reads before it waits for this one
+    // was complete here.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Pair w = find_pair(p, ts, blockIdx.x, lane);
     if (!w.any) return;   // block-uniform, before tensor memory is allocated
     const int b = w.b, len = w.len, g = w.g, t0 = w.t0, t1 = w.t1, h0 = w.h0, h1 = w.h1;
@@ -1070,11 +1073,13 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
-    pdl_wait();
     const int rank = blockIdx.x % ns, cluster = blockIdx.x / ns;   // the cluster's CTAs take every ns-th head
     const int g = cluster % p.kv_heads, group = p.heads / p.kv_heads;
     int b, len, t;
-    if (!find_tile<false>(p, ts, cluster / p.kv_heads, lane, &b, &len, &t)) return;   // cluster-uniform, before tensor memory is allocated
+    if (!find_tile<false>(p, ts, cluster / p.kv_heads, lane, &b, &len, &t)) {   // cluster-uniform, before tensor memory is allocated
+        pdl_wait();   // nor may this kernel end before the one ahead of it
+        return;
+    }
     const int tiles = (len + TILE - 1) / TILE;
     const int heads = (group - rank + ns - 1) / ns;
     const int units = (tiles - t) * heads;   // unit n: query tile t + n / heads, head rank + n % heads ns of the group
@@ -1112,6 +1117,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     if (!partial) mbar_arrive_expect_tx(gb, TB);
                     load_tile<D>(dg, &tmG, gb, h * D, row);
                 }
+                if (n == 0) pdl_wait();   // delta and lse2 are the gradient of q's; all else was there before it
                 float *st = stats + s * 2 * TILE;
 #pragma unroll
                 for (int e = lane; e < TILE; e += 32) {
