@@ -169,10 +169,12 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, 
 // the tile's rows would multiply by a zero probability; 0 times infinity or NaN is not zero.
 template <int D>
 __device__ __forceinline__ void clear_rows(uint8_t *tile, int row, int lane) {
+    const uint32_t base = smem_u32(tile);
+#pragma unroll 4
+    for (int i = row * 128 + lane * 16; i < BOX_BYTES; i += 512)
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b)
-        for (int i = row * 8 + lane; i < TILE * 8; i += 32)
-            *reinterpret_cast<uint4 *>(tile + b * BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < D / 64; ++b)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(base + b * BOX_BYTES + i), "r"(0) : "memory");
     fence_proxy_async_smem();
     __syncwarp();
 }
@@ -774,25 +776,26 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 const int row = b + j * TILE, rows = len - j * TILE;
                 uint8_t *dst = sk + (j & 1) * TB;
                 if (!(ok = warp_all(mbar_wait(&k_empty[j & 1], ((j >> 1) & 1) ^ 1)))) break;
-                if (rows < TILE) {   // the sequence's last K tile
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(tail, TB);
-                        load_tile<D>(dst, &tmK, tail, g * D, row);
-                    }
-                    if (!(ok = warp_all(mbar_wait(tail, 0)))) break;
-                    clear_rows<D>(dst, rows, lane);
-                    if (lane == 0) mbar_arrive(&k_full[j & 1]);
-                } else if (lane == 0) {
-                    mbar_arrive_expect_tx(&k_full[j & 1], TB);
-                    load_tile<D>(dst, &tmK, &k_full[j & 1], g * D, row);
-                }
-                ++nk;
-                if (!(ok = warp_all(mbar_wait(v_empty, (j & 1) ^ 1)))) break;
+                const bool partial = rows < TILE;   // the sequence's last K tile
+                uint64_t *kb = partial ? tail : &k_full[j & 1];
                 if (lane == 0) {
+                    mbar_arrive_expect_tx(kb, TB);
+                    load_tile<D>(dst, &tmK, kb, g * D, row);
+                }
+                const bool v_free = warp_all(mbar_wait(v_empty, (j & 1) ^ 1));
+                if (v_free && lane == 0) {
                     mbar_arrive_expect_tx(v_full, TB);
                     load_tile<D>(sv, &tmV, v_full, g * D, row);
                 }
-                ++nv;
+                nv += v_free;
+                if (partial) {
+                    if (!(ok = warp_all(mbar_wait(tail, 0)))) break;
+                    clear_rows<D>(dst, rows, lane);
+                    if (lane == 0) mbar_arrive(&k_full[j & 1]);
+                }
+                ++nk;
+                ok = v_free;
+                if (!ok) break;
             }
             // every copy lands before the CTA may leave
             mbar_wait(q_full, 0);
