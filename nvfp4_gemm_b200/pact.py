@@ -156,10 +156,10 @@ def _check(status: int):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, dev: Optional[int] = None) -> Optional[int]:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -639,13 +639,23 @@ def _on(t: torch.Tensor, name: str, dtype, dev: int, shape=None) -> torch.Tensor
     return t
 
 
+# The current device without the check that CUDA is up, which a CUDA tensor settles.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _device(t: torch.Tensor) -> int:
     """The current device (without asking for one on behalf of a host tensor, which _on refuses)."""
-    return torch.cuda.current_device() if t.is_cuda else -1
+    return _current_device() if t.is_cuda else -1
 
 
 def _matrix(t: torch.Tensor, name: str, dev: int, shape=None) -> int:
     """The row stride of a BF16 matrix (of this shape) with contiguous rows."""
+    if t.dtype is torch.bfloat16 and t.get_device() == dev >= 0:   # most calls: few questions to the tensor
+        stride = t.stride()
+        if len(stride) == 2 and stride[1] == 1:
+            have = t.shape
+            if have[0] > 1 and (shape is None or have == shape):
+                return stride[0]
     _on(t, name, torch.bfloat16, dev, shape)
     if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
         raise ValueError(f"{name}: expected a matrix with contiguous rows")
@@ -698,7 +708,7 @@ def pact_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: Sequence[float
         y = _new((M, cols), torch.bfloat16, x.device, stream)
     ldy = _matrix(y, "y", dev, (M, cols))
     _check(_lib.pact_rope(x.data_ptr(), ldx, M, heads, 2 * half, positions.data_ptr(), inv_freq.data_ptr(),
-                          int(bool(inverse)), y.data_ptr(), ldy, _stream(stream)))
+                          int(bool(inverse)), y.data_ptr(), ldy, _stream(stream, dev)))
     return y
 
 
@@ -737,7 +747,7 @@ def pact_attention_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, seq_st
         lse = _new((heads, a.M), torch.float32, q.device, stream)
     ldo = _matrix(o, "o", dev, q.shape)
     _check(_lib.pact_attention_fwd(ctypes.byref(a), o.data_ptr(), ldo, _lse(lse, dev, (heads, a.M)).data_ptr(),
-                                   _stream(stream)))
+                                   _stream(stream, dev)))
     return o, lse
 
 
@@ -761,7 +771,7 @@ def pact_attention_bwd(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                          dv.data_ptr(), _matrix(dv, "dv", dev, v.shape))
     ws = _scratch(workspace, lambda: pact_attention_bwd_workspace_bytes(a.M, heads), q.device, dev, stream)
     _check(_lib.pact_attention_bwd(ctypes.byref(a), ctypes.byref(g), ws.data_ptr(), ws.numel() * ws.element_size(),
-                                   _stream(stream)))
+                                   _stream(stream, dev)))
     return dq, dk, dv
 
 
