@@ -441,7 +441,7 @@ PACT_API pact_status pact_rmsnorm_bwd(const pact_bf16 *dy, int64_t lddy, const p
  * BF16.  inverse != 0 rotates by -t: the gradient (the transpose) of the rotation.
  * x [M x heads*head_dim] (row stride ldx; e.g. the q and k columns of a q|k|v output),
  * y likewise (row stride ldy); y may be x itself with the same stride, and otherwise
- * must not overlap it.  positions: M int32; a negative one marks a row of padding,
+ * must not overlap it (refused where it is seen to).  positions: M int32; a negative one marks a row of padding,
  * which is not written.  inv_freq: HOST array of head_dim/2 doubles, read before the
  * call returns.  head_dim is 64 or 128. */
 PACT_API pact_status pact_rope(const pact_bf16 *x, int64_t ldx, int64_t M, int heads, int head_dim,
@@ -478,7 +478,7 @@ typedef struct {
  * not finite may reach every row of its own sequence.  seq_start is read on the device:
  * numbers outside [0, M] are taken as the nearest end, and where they decrease the rows
  * concerned are unspecified (no access leaves the M rows).  Outputs must not overlap
- * the inputs. */
+ * the inputs (for matrices of one row stride it is checked; columns side by side do not). */
 PACT_API pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o, int64_t ldo, float *lse,
                                         pact_stream_t stream);
 

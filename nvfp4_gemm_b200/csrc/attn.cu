@@ -386,10 +386,11 @@ static_assert(2 * 128 * 216 + 128 * 72 <= SPLIT_THREADS * 168, "more registers t
 // also knows its accumulator at rest.  The CTA is persistent: the next pair's Q, K and scores
 // come under the last pair's output.
 // Rounding: P to BF16, as the MMA takes it (by at most 2^-8 of a probability); the row sums add the FP32 values.
-// 4 x 2048 tokens, 24 and 8 heads of 128: 121 us, 849 TFLOP/s of the 103 GFLOP under the diagonal (51% of
+// 4 x 2048 tokens, 24 and 8 heads of 128: 118 us, 871 TFLOP/s of the 103 GFLOP under the diagonal (52% of
 // the measured BF16 rate).  A block of a pair takes 3000 cycles for 2048 of MMAs: a unit's softmax takes
 // 1500 (1024 of them the special-function units'), and with two units in tensor memory it is not
-// wholly under the other's products.
+// wholly under the other's products.  Tried without gain: sixteen softmax warps, two threads a row that
+// exchange their maxima (3% slower), and with them a share of the exponentials on the FP32 units (more so).
 namespace fwd {
 constexpr int STAGES = 4;
 template <int D>
@@ -676,7 +677,8 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // dq has a kernel of its own, with S and dP formed a second time for dk and dv (7 products
 // instead of 5): summing dq over key tiles from one kernel takes atomics in FP32, whose
 // order would change the result from call to call, and a pass to clear and round it.
-// This kernel also leaves delta and lse log2(e) for the other one.
+// This kernel also leaves delta and lse log2(e) for the other one, which is launched while this one
+// runs, loads its first tiles and waits with those two alone (some 2 us a call).
 // Rounding: dS to BF16, as the MMA takes it; P, dP and the sums stay FP32.
 // 4 x 2048 tokens, 24 and 8 heads of 128: some 185 us (three products: 37% of the measured BF16 rate).  A
 // block of a pair takes 4700 cycles for 48 MMAs of 64; the tensor core waits for dS, 1400 cycles after dP.

@@ -17,7 +17,9 @@
 // memory (k_muon_fused): u stays in shared memory between its Gram matrix and P u.  Its phases
 // (load, Gram matrix, P, P u, store) follow one another in a CTA and overlap only between the two
 // CTAs of an SM: the 392 adapter matrices of 28 layers (rank 16, 406 MB) take 126 us, 3.2 TB/s or
-// 49% of the measured copy rate, the 14 of one layer 18.  Larger ones take three kernels:
+// 49% of the measured copy rate, the 14 of one layer 18.  Tried: whole float4s of u through shared memory
+// (4% slower), clusters of sixteen with three or four CTAs an SM (10 to 30% slower), a later CTA's g and m
+// asked into L2 ahead of it (3% faster, not worth its code).  Larger ones take three kernels:
 //   k_muon_gram   a slab of the long side per CTA: m' is written, the slab's part of
 //                 u u^T goes to scratch
 //   k_muon_poly   one CTA per matrix: S0 from the parts in a fixed order, then P
