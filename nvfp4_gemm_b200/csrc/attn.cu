@@ -58,11 +58,21 @@ __device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
 // ... and by the FP32 units: x = n + f with n the nearest whole number (adding 1.5 2^23
 // rounds it into the low bits), 2^f by the polynomial of degree 4 with the least relative
 // error on [-1/2, 1/2] (Remez exchange: 2.6e-6, under the BF16 rounding of a probability by
-// a factor of 700), n added to the exponent.  Below -126 it gives about 2^-126.
+// a factor of 700), n added to the exponent.  Below -126 it gives about 2^-126.  A NaN would
+// come out as a finite number (the maximum drops it, and n added to its bits would do the
+// same); with NANS the maximum keeps it and 2^n enters as a factor.  dk and dv need that.  dq does
+// not: P is NaN there only where the row's lse is, whose o and so delta are NaN too, and dS =
+// P (dP - delta) with them (at 4 x 2048 tokens with heads of 64 NANS would cost dq 10 us of 349).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+template <bool NANS>
 __device__ __forceinline__ uint64_t ex2_fma(uint64_t x) {
     float a, b;
     f2_unpack(x, a, b);
-    x = f2_pack(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+    x = NANS ? f2_pack(max_nan(a, -126.0f), max_nan(b, -126.0f)) : f2_pack(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
     const uint64_t magic = f2_pack(12582912.0f, 12582912.0f), minus = f2_pack(-12582912.0f, -12582912.0f);
     const uint64_t t = f2_add(x, magic), n = f2_add(t, minus);
     const uint64_t f = f2_fma(n, f2_pack(-1.0f, -1.0f), x);
@@ -70,12 +80,15 @@ __device__ __forceinline__ uint64_t ex2_fma(uint64_t x) {
     y = f2_fma(f, y, f2_pack(0.240247448f, 0.240247448f));
     y = f2_fma(f, y, f2_pack(0.693121815f, 0.693121815f));
     y = f2_fma(f, y, f2_pack(0.999999261f, 0.999999261f));
-    const uint32_t lo = (uint32_t)y + ((uint32_t)t << 23), hi = (uint32_t)(y >> 32) + ((uint32_t)(t >> 32) << 23);
-    return (uint64_t)hi << 32 | lo;
+    const uint64_t base = NANS ? f2_pack(1.0f, 1.0f) : y;
+    const uint32_t lo = (uint32_t)base + ((uint32_t)t << 23), hi = (uint32_t)(base >> 32) + ((uint32_t)(t >> 32) << 23);
+    const uint64_t scaled = (uint64_t)hi << 32 | lo;
+    return NANS ? f2_mul(y, scaled) : scaled;
 }
-// Of EX2_PERIOD pairs, this many go to the FP32 units.  Gradients over 4 x 2048 tokens, 24 and 8 heads of 128:
-// 355 us with none, 348 so, 362 with half of dk and dv's.  The forward gains nothing (114 us with
-// none, one or two, 120 with three).
+// Of EX2_PERIOD pairs, this many go to the FP32 units.  Gradients over 4 x 2048 tokens, cold L2, 24 and 8
+// heads of 128: 390 us with none, 384 so, 388 with half of dq's, 396 with half of dk and dv's; 32
+// and 8 heads of 64: 355, 349, 365, 367.  The forward gains nothing (heads of 128, 114 us with none,
+// one or two, 120 with three).
 constexpr int EX2_PERIOD = 8, EX2_BY_FMA_DQ = 2, EX2_BY_FMA_DKV = 1;
 
 // 128 columns of a lane.
@@ -917,7 +930,7 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
                 const uint64_t x = f2_fma((uint64_t)r[2 * e + 1] << 32 | r[2 * e], c2, m2);
-                pr[e] = e % EX2_PERIOD < EX2_BY_FMA_DQ ? ex2_fma(x) : ex2_pair(x);
+                pr[e] = e % EX2_PERIOD < EX2_BY_FMA_DQ ? ex2_fma<false>(x) : ex2_pair(x);
             }
             if (!(ok = warp_all(mbar_wait(&dp_full[u], j & 1)))) break;
             tc_fence_after();
@@ -1227,7 +1240,7 @@ k_attn_dkv(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 #pragma unroll
                     for (int k = e; k < e + 2; ++k) {
                         const uint64_t x = f2_fma((uint64_t)r[hf][2 * k + 1] << 32 | r[hf][2 * k], c2, k == e ? ls.x : ls.y);
-                        pr[hf][k] = k % EX2_PERIOD < EX2_BY_FMA_DKV ? ex2_fma(x) : ex2_pair(x);
+                        pr[hf][k] = k % EX2_PERIOD < EX2_BY_FMA_DKV ? ex2_fma<true>(x) : ex2_pair(x);
                     }
                 }
                 if (edge) clear_edge(pr[hf], first - 64 * hf, end - 64 * hf);

@@ -279,3 +279,27 @@ def test_many_sequences_between_padding(hq, hk, D):
         assert torch.equal(got[rows], ref)
         assert bool((got[:ahead] == -7.0).all() and (got[ahead + M:] == -7.0).all())
     assert bool((lse2[:, :ahead] == -7.0).all() and (lse2[:, ahead + M:] == -7.0).all())
+
+
+@pytest.mark.parametrize("at", [0, 1, 5, 16, 17, 31, 144])
+@pytest.mark.parametrize("lens", [[1], [1, 40, 200]], ids=str)
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_query_that_is_not_finite_shows_in_its_gradients(D, lens, at):
+    """A NaN in one query row: its own dq, and dk and dv of every key it sees, are NaN wherever it lies in
+    its tile; the other sequences stay finite."""
+    import nvfp4_gemm_b200 as P
+    hq, hk, head = 4, 2, 1
+    q, k, v, cu, starts, M = problem(lens, 0, hq, hk, D)
+    do = bf(2, M, hq * D)
+    a, b = starts[-2], M          # the last sequence
+    row = a + min(at, b - a - 1)
+    q[row, head * D] = math.nan
+    o, lse = P.pact_attention_fwd(q, k, v, cu, hq, hk)
+    own, group = slice(head * D, (head + 1) * D), slice(0, D)
+    assert bool(o[row, own].isnan().all() and lse[head, row].isnan())
+    dq, dk, dv = P.pact_attention_bwd(do, q, k, v, o, lse, cu, hq, hk)
+    status_ok()
+    assert bool(dq[row, own].isnan().all()), "dq"
+    for name, t in (("dk", dk), ("dv", dv)):
+        assert bool(t[a:row + 1, group].isnan().all()), name
+        assert bool(t[:a].isfinite().all() and t[:, D:].isfinite().all()), name
