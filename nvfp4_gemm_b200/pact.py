@@ -663,19 +663,31 @@ def _matrix(t: torch.Tensor, name: str, dev: int, shape=None) -> int:
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream`, from that stream's own pool: the current stream's may hand out a block
+    that work still pending there reads or writes."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # a raw handle; 0 and 1 are the default stream's
+        stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
+                  else torch.cuda.ExternalStream(int(stream), device=device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor a call allocates for itself.  Its memory belongs to the current stream; where the call runs on
-    another one, the allocator is told, so that freeing it does not hand it out while that stream still uses it."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+    """An output a call on `stream` allocates.  The caller's stream will read it, so the allocator is told: once
+    freed, it is not handed out again before that stream is through with it."""
+    t = _empty(shape, dtype, device, stream)
     if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+        t.record_stream(torch.cuda.current_stream())
     return t
 
 
 def _scratch(ws: Optional[torch.Tensor], need, device, dev: int, stream) -> torch.Tensor:
     """The caller's workspace (the library checks its size and alignment), or need() bytes of the call's own."""
     if ws is None:
-        return _new(need(), torch.uint8, device, stream)
+        return _empty(need(), torch.uint8, device, stream)
     if not ws.is_cuda:
         raise TypeError("workspace: expected a CUDA tensor")
     if ws.get_device() != dev:

@@ -210,3 +210,49 @@ def test_an_updated_layer_is_the_layer_of_the_new_adapters(monkeypatch):
         assert torch.equal(getattr(L, name), getattr(fresh, name)), name
     for k in L.grads:
         assert torch.equal(L.grads[k], fresh.grads[k]), k
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_memory_for_another_stream_is_not_the_current_streams(raw):
+    """A call on another stream takes neither its outputs nor its scratch from a block that was just freed on
+    the current stream while work is pending there."""
+    import nvfp4_gemm_b200 as P
+    M, hq, hk, D = 512, 4, 2, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    bf = lambda n: torch.randn((M, n), generator=g, device="cuda").bfloat16()
+    q, k, v, do = bf(hq * D), bf(hk * D), bf(hk * D), bf(hq * D)
+    cu = torch.tensor([0, 200, M], dtype=torch.int32, device="cuda")
+    pos = torch.arange(M, dtype=torch.int32, device="cuda")
+    freq = [1e4 ** (-2 * i / D) for i in range(D // 2)]
+    w, grad = torch.randn((64, 3000), generator=g, device="cuda"), torch.randn((64, 3000), generator=g, device="cuda")
+
+    def calls(stream):
+        o, lse = P.pact_attention_fwd(q, k, v, cu, hq, hk, stream=stream)
+        w1, m1 = w.clone(), torch.zeros_like(w)
+        torch.cuda.current_stream().synchronize()      # the copies, before the other stream updates them
+        return [lambda: [P.pact_rope(q, pos, freq, hq, stream=stream)],
+                lambda: list(P.pact_attention_fwd(q, k, v, cu, hq, hk, stream=stream)),
+                lambda: list(P.pact_attention_bwd(do, q, k, v, o, lse, cu, hq, hk, stream=stream)),
+                lambda: [P.pact_muon_step([w1], [grad], [m1], lr=0.1, stream=stream), w1, m1][1:]]
+    want = [f() for f in calls(None)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    todo = calls(side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
+    sizes = [M * hq * D * 2, M * hk * D * 2, M * hq * 4, P.pact_attention_bwd_workspace_bytes(M, hq),
+             P.pact_muon_workspace_bytes([w.shape])]
+    for f, ref in zip(todo, want):
+        blocks = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(3)]
+        kept = [torch.empty_like(b) for b in blocks]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)       # some 25 ms of the current stream, ahead of its reads of the blocks
+        for a, b in zip(kept, blocks):
+            a.copy_(b)
+        begin = {b.data_ptr() for b in blocks}
+        del blocks, b
+        got = f()
+        side.synchronize()
+        assert not begin & {t.data_ptr() for t in got}
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
+        assert all(bool((a == 7).all()) for a in kept)
