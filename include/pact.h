@@ -532,9 +532,10 @@ typedef struct {
 } pact_muon_matrix_t;
 /* mats: HOST array of n such entries, read before the call returns; pointers aligned to
  * their elements (16-byte aligned ones with cols a multiple of 4 are read faster).
- * Matrices must not overlap one another (outputs that do are refused).  workspace: device, 16-byte aligned, >=
- * pact_muon_workspace_bytes(mats, n) (which reads count, rows and cols only); calls that share
- * it must not overlap on the GPU. */
+ * Outputs must not overlap one another, nor an input or the workspace, but for a momentum_out
+ * or weight_out that is its own momentum or weight (refused otherwise); inputs may.
+ * workspace: device, 16-byte aligned, >= pact_muon_workspace_bytes(mats, n) (which reads count, rows
+ * and cols only); calls that share it must not overlap on the GPU. */
 PACT_API size_t pact_muon_workspace_bytes(const pact_muon_matrix_t *mats, int n);
 PACT_API pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32, double lr,
                                     double momentum, double weight_decay, int nesterov, void *workspace,

@@ -634,15 +634,23 @@ pact_status pact_muon_step(const pact_muon_matrix_t *mats, int n, int grad_fp32,
     PACT_CHECK(workspace && ws_bytes >= pact_muon_workspace_bytes(mats, n), PACT_ERR_INVALID_ARG,
                "%s: workspace too small", what);
     PACT_CHECK(aligned16(workspace), PACT_ERR_ALIGN, "%s: workspace must be 16-byte aligned", what);
-    // a matrix given twice would be updated by two CTAs at once
-    Ranges written(3 * (int64_t)n);
+    // A matrix given twice would be updated by two CTAs at once, and what is read must not change under the
+    // call: a gradient, for one, is read again after the momentum is written where a matrix takes three
+    // kernels.  Only a momentum or weight that is its own output may be both.
+    Ranges all(6 * (int64_t)n + 1);
     for (int i = 0; i < n; ++i) {
-        const int64_t size = mats[i].count * mats[i].rows * mats[i].cols;
-        written.add(mats[i].momentum_out, 4 * size);
-        written.add(mats[i].weight_out, 4 * size);
-        written.add(mats[i].weight_bf16, 2 * size);
+        const pact_muon_matrix_t &m = mats[i];
+        const int64_t size = m.count * m.rows * m.cols;
+        all.add(m.momentum_out, 4 * size, true);
+        all.add(m.weight_out, 4 * size, true);
+        all.add(m.weight_bf16, 2 * size, true);
+        all.add(m.grad, (grad_fp32 ? 4 : 2) * size, false);
+        if (m.momentum != m.momentum_out) all.add(m.momentum, 4 * size, false);
+        if (m.weight != m.weight_out) all.add(m.weight, 4 * size, false);
     }
-    PACT_CHECK(written.disjoint(), PACT_ERR_INVALID_ARG, "%s: outputs overlap (a matrix given twice?)", what);
+    all.add(workspace, (int64_t)pact_muon_workspace_bytes(mats, n), true);
+    PACT_CHECK(all.disjoint(), PACT_ERR_INVALID_ARG,
+               "%s: an output or the workspace overlaps another output (a matrix given twice?) or an input", what);
     int rmax = 1;
     for (int i = 0; i < n; ++i) rmax = std::max(rmax, (int)std::min(mats[i].rows, mats[i].cols));
     const int nb = blocks_of(rmax);

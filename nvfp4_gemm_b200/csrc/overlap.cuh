@@ -32,23 +32,29 @@ inline bool overlap_any(const Rows *m, int outs, int n, int64_t rows) {
     return false;
 }
 
-// Byte ranges collected one by one, then compared all at once.
+// Byte ranges that a call writes or only reads, collected one by one, then compared all at once.
 struct Ranges {
     struct Range {
         uintptr_t begin, end;
+        bool written;
     };
     std::unique_ptr<Range[]> r;   // not a vector: nothing may be thrown through a C entry
     int64_t n = 0;
     explicit Ranges(int64_t most) : r(new (std::nothrow) Range[most]) {}
-    void add(const void *p, int64_t bytes) {
-        if (r && p) r[n++] = {(uintptr_t)p, (uintptr_t)p + bytes};
+    void add(const void *p, int64_t bytes, bool written) {
+        if (r && p) r[n++] = {(uintptr_t)p, (uintptr_t)p + bytes, written};
     }
-    // Sorts them; false without host memory for the list, too.
+    // Whether no written range overlaps another one (ranges that are only read may).  Sorts them; false
+    // without host memory for the list, too.
     bool disjoint() {
         if (!r) return false;
         std::sort(&r[0], &r[0] + n, [](const Range &a, const Range &b) { return a.begin < b.begin; });
-        for (int64_t i = 1; i < n; ++i)
-            if (r[i].begin < r[i - 1].end) return false;
+        uintptr_t written = 0, any = 0;   // ends of the ranges before
+        for (int64_t i = 0; i < n; ++i) {
+            if (r[i].begin < (r[i].written ? any : written)) return false;
+            any = std::max(any, r[i].end);
+            if (r[i].written) written = std::max(written, r[i].end);
+        }
         return true;
     }
 };

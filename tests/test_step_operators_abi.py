@@ -154,3 +154,43 @@ def test_a_matrix_given_twice_is_refused(P):
             other[k] = one[k] + shift
             assert call(one, other) == call(other, one) == INVALID and "twice" in P.pact_last_error()
     assert call([0x1000, 0x100000, 0x100000, 0x200000, 0x100000, None]) == INVALID
+
+
+@pytest.mark.parametrize("fp32", [0, 1])
+def test_an_update_over_its_inputs_is_refused(P, fp32):
+    """But for a momentum or weight updated in place, no output may share memory with what the call reads."""
+    lib, c = P.pact.lib, P.pact.c_muon_matrix
+    rows, cols = 16, 300
+    size, gsize = 4 * rows * cols, (4 if fp32 else 2) * rows * cols
+    ws = 0x4000000
+
+    def call(*at, ws=ws):
+        m = (c * len(at))(*[c(*a, 1, rows, cols) for a in at])
+        return lib.pact_muon_step(m, len(at), fp32, 0.1, 0.9, 0.0, 1, ws, lib.pact_muon_workspace_bytes(m, len(at)), None)
+    #       grad      momentum  its output weight   its output BF16 copy
+    one = [0x100000, 0x200000, 0x300000, 0x400000, 0x500000, 0x600000]
+    two = [p + 0x1000000 for p in one]
+    # What is no overlap passes the check.  Only without a device, where the launch behind it fails: these
+    # addresses are none of its memory.
+    if not torch.cuda.is_available():
+        for fine in ((one, two), ([one[0], one[1], one[1], one[3], one[3], one[5]], two), (one, [one[0]] + two[1:]),
+                     (one, [two[0], one[1], two[2], one[3], *two[4:]])):
+            assert call(*fine) != INVALID, P.pact_last_error()
+    outs, ins = (2, 4, 5), (0, 1, 3)
+    for o in outs:
+        for i in ins:
+            far = gsize if i == 0 else size
+            for shift in (0, 16, far - 16):
+                if shift == 0 and (o, i) in ((2, 1), (4, 3)):
+                    continue                      # in place
+                same, other = list(one), list(two)
+                same[o] = one[i] + shift          # the entry's own input
+                other[o] = one[i] + shift         # another entry's
+                assert call(same, two) == INVALID and "overlap" in P.pact_last_error()
+                assert call(one, other) == call(other, one) == INVALID
+        at = list(two)
+        at[o] = one[1]
+        assert call(one, at) == INVALID           # another entry's momentum, whole
+        assert call(one, two, ws=one[o] - 16) == INVALID
+    for i in ins:
+        assert call(one, two, ws=two[i] - 16) == INVALID
