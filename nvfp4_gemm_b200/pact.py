@@ -710,7 +710,7 @@ def pact_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: Sequence[float
     _on(positions, "positions", torch.int32, dev, (M,))
     if positions.stride(0) != 1 and M > 1:
         raise ValueError("positions: expected a contiguous vector")
-    half = cols // heads // 2
+    D, half = cols // heads, cols // heads // 2
     if len(inv_freq) != half:
         raise ValueError(f"inv_freq: {len(inv_freq)} values, expected {half}")
     if not (isinstance(inv_freq, torch.Tensor) and inv_freq.dtype == torch.float64 and not inv_freq.is_cuda
@@ -719,7 +719,7 @@ def pact_rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: Sequence[float
     if y is None:
         y = _new((M, cols), torch.bfloat16, x.device, stream)
     ldy = _matrix(y, "y", dev, (M, cols))
-    _check(_lib.pact_rope(x.data_ptr(), ldx, M, heads, 2 * half, positions.data_ptr(), inv_freq.data_ptr(),
+    _check(_lib.pact_rope(x.data_ptr(), ldx, M, heads, D, positions.data_ptr(), inv_freq.data_ptr(),
                           int(bool(inverse)), y.data_ptr(), ldy, _stream(stream, dev)))
     return y
 

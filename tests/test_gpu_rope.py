@@ -72,3 +72,14 @@ def test_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, P.pact_rope(x, pos, freqs(64), 8))
+
+
+@pytest.mark.parametrize("heads,D", [(8, 65), (8, 129), (16, 127), (4, 96), (4, 32)])
+def test_other_head_sizes_are_refused(heads, D):
+    """Odd ones too: 65 columns a head are not heads of 64."""
+    import nvfp4_gemm_b200 as P
+    x, pos = bf(1, 4, heads * D), torch.arange(4, device="cuda", dtype=torch.int32)
+    y = torch.full_like(x, 7.0)
+    with pytest.raises(P.PactError):
+        P.pact_rope(x, pos, [0.0] * (D // 2), heads, y=y)
+    assert bool((y == 7.0).all())
