@@ -440,9 +440,9 @@ PACT_API pact_status pact_rmsnorm_bwd(const pact_bf16 *dy, int64_t lddy, const p
  * in FP32 with t reduced in FP64 (far positions keep their angle), rounded once to
  * BF16.  inverse != 0 rotates by -t: the gradient (the transpose) of the rotation.
  * x [M x heads*head_dim] (row stride ldx; e.g. the q and k columns of a q|k|v output),
- * y likewise (row stride ldy); y may be x itself with the same stride, and otherwise
- * must not overlap it (refused where it is seen to).  positions: M int32; a negative one marks a row of padding,
- * which is not written.  inv_freq: HOST array of head_dim/2 doubles, read before the
+ * y likewise (row stride ldy); y may be x itself with the same stride; otherwise
+ * an overlap with x, as one with positions, is refused.  positions: M int32; a negative one
+ * marks a row of padding, which is not written.  inv_freq: HOST array of head_dim/2 doubles, read before the
  * call returns.  head_dim is 64 or 128. */
 PACT_API pact_status pact_rope(const pact_bf16 *x, int64_t ldx, int64_t M, int heads, int head_dim,
                                const int32_t *positions, const double *inv_freq, int inverse, pact_bf16 *y,
@@ -477,8 +477,8 @@ typedef struct {
  * not depend on other sequences or on rows of none, whatever they hold; a value that is
  * not finite may reach every row of its own sequence.  seq_start is read on the device:
  * numbers outside [0, M] are taken as the nearest end, and where they decrease the rows
- * concerned are unspecified (no access leaves the M rows).  Outputs must not overlap
- * the inputs (for matrices of one row stride it is checked; columns side by side do not). */
+ * concerned are unspecified (no access leaves the M rows).  Outputs that overlap one another
+ * or an input are refused (columns of one buffer, side by side, do not overlap). */
 PACT_API pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o, int64_t ldo, float *lse,
                                         pact_stream_t stream);
 
@@ -487,10 +487,10 @@ PACT_API pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o,
  *   dq_i = scale sum_j dS_ij k_j;  dk_j = scale sum dS_ij q_i,  dv_j = sum P_ij do_i  over
  *   the rows i and the query heads of j's group.
  * P and dS enter their products as BF16; every sum is FP32 in a fixed order (repeated
- * calls agree bit for bit).  Rows of no sequence are left as they were; outputs must not
- * overlap the inputs.  workspace
- * (device, 16-byte aligned, >= pact_attention_bwd_workspace_bytes(M, heads)) is scratch;
- * calls that share it must not overlap on the GPU. */
+ * calls agree bit for bit).  Rows of no sequence are left as they were; outputs and a
+ * workspace that overlap one another or an input are refused.  workspace (device, 16-byte aligned,
+ * >= pact_attention_bwd_workspace_bytes(M, heads)) is scratch; calls that share it must not
+ * overlap on the GPU. */
 typedef struct {
     const pact_bf16 *o;        /* [M x heads*head_dim] as written by the forward */
     int64_t ldo;

@@ -1443,8 +1443,11 @@ pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o, int64_t 
                "pact_attention_fwd: o needs 16-byte aligned rows of at least %lld elements, lse 16-byte alignment",
                (long long)nq);
     const int64_t nk = (int64_t)a->kv_heads * a->head_dim;
-    const Rows all[] = {{o, ldo, nq}, {a->q, a->ldq, nq}, {a->k, a->ldk, nk}, {a->v, a->ldv, nk}};
-    PACT_CHECK(!overlap_any(all, 1, 4, a->M), PACT_ERR_INVALID_ARG, "pact_attention_fwd: o overlaps q, k or v");
+    const int64_t M = a->M;
+    const Rows all[] = {matrix(o, ldo, nq, M),         memory(lse, 4 * M * a->heads),  matrix(a->q, a->ldq, nq, M),
+                        matrix(a->k, a->ldk, nk, M),   matrix(a->v, a->ldv, nk, M),    memory(a->seq_start, 4 * (a->nseq + 1))};
+    PACT_CHECK(!overlap_any(all, 2, 6), PACT_ERR_INVALID_ARG,
+               "pact_attention_fwd: o or lse overlaps the other, q, k, v or seq_start");
     attn::Params p = attn::base(a);
     p.o = o; p.ldo = ldo; p.lse = lse;
     return a->head_dim == 64 ? attn::run_fwd<64>(p, (cudaStream_t)stream) : attn::run_fwd<128>(p, (cudaStream_t)stream);
@@ -1469,10 +1472,20 @@ pact_status pact_attention_bwd(const pact_attention_t *a, const pact_attention_g
                    attn::row_ok(g->dq, g->lddq, nq) && attn::row_ok(g->dk, g->lddk, nk) &&
                    attn::row_ok(g->dv, g->lddv, nk) && aligned16(g->lse) && aligned16(workspace),
                PACT_ERR_ALIGN, "%s: rows must be 16-byte aligned with leading dimensions at least their width", what);
-    const Rows all[] = {{g->dq, g->lddq, nq}, {g->dk, g->lddk, nk}, {g->dv, g->lddv, nk},       {a->q, a->ldq, nq},
-                        {a->k, a->ldk, nk},   {a->v, a->ldv, nk},   {g->o, g->ldo, nq}, {g->dout, g->lddout, nq}};
-    PACT_CHECK(!overlap_any(all, 3, 8, a->M), PACT_ERR_INVALID_ARG,
-               "%s: dq, dk or dv overlap one another or an input", what);
+    const int64_t M = a->M;
+    const Rows all[] = {matrix(g->dq, g->lddq, nq, M),
+                        matrix(g->dk, g->lddk, nk, M),
+                        matrix(g->dv, g->lddv, nk, M),
+                        memory(workspace, (int64_t)pact_attention_bwd_workspace_bytes(M, a->heads)),
+                        matrix(a->q, a->ldq, nq, M),
+                        matrix(a->k, a->ldk, nk, M),
+                        matrix(a->v, a->ldv, nk, M),
+                        matrix(g->o, g->ldo, nq, M),
+                        matrix(g->dout, g->lddout, nq, M),
+                        memory(g->lse, 4 * M * a->heads),
+                        memory(a->seq_start, 4 * (a->nseq + 1))};
+    PACT_CHECK(!overlap_any(all, 4, 11), PACT_ERR_INVALID_ARG,
+               "%s: dq, dk, dv or the workspace overlap one another or an input", what);
     attn::Params p = attn::base(a);
     p.o_in = g->o; p.ldo = g->ldo; p.dout = g->dout; p.lddo = g->lddout;
     p.lse = const_cast<float *>(g->lse);

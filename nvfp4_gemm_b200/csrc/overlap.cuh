@@ -5,30 +5,41 @@
 #include <cstdint>
 #include <memory>
 #include <new>
+#include <numeric>
 
 #include "common.cuh"
 
 namespace pact {
 
-struct Rows {   // a matrix of `rows` rows of the call, in BF16
-    const pact_bf16 *p;
-    int64_t ld, cols;
+struct Rows {   // `rows` rows of `width` bytes, `ld` bytes from one to the next
+    uintptr_t p;
+    int64_t ld, width, rows;
 };
+inline Rows matrix(const pact_bf16 *p, int64_t ld, int64_t cols, int64_t rows) {
+    return {(uintptr_t)p, 2 * ld, 2 * cols, rows};
+}
+inline Rows memory(const void *p, int64_t bytes) { return {(uintptr_t)p, bytes, bytes, 1}; }
 
-// Whether the later matrix's first row lies in the earlier one's rows: the answer for matrices of one row
-// stride (columns of one buffer may lie side by side), and a lower bound of it for others.
-inline bool overlap(Rows a, Rows b, int64_t rows) {
-    if ((uintptr_t)a.p > (uintptr_t)b.p) std::swap(a, b);
-    const int64_t d = (int64_t)(((uintptr_t)b.p - (uintptr_t)a.p) / sizeof(pact_bf16));
-    if (d >= (rows - 1) * a.ld + a.cols) return false;
-    return d % a.ld < a.cols || (d % a.ld + b.cols > a.ld && d / a.ld + 1 < rows);
+// Whether two sets of rows share a byte (columns of one buffer may lie side by side).  Each row of the later
+// one that starts between the ends of the earlier one is looked up there; they come to lie at
+// columns that repeat, from earlier rows on, after ld / gcd of the two strides.
+inline bool overlap(Rows a, Rows b) {
+    if (a.p > b.p) std::swap(a, b);
+    const int64_t extent = (a.rows - 1) * a.ld + a.width, d = (int64_t)(b.p - a.p);
+    if (d >= extent) return false;
+    const int64_t rows = std::min(b.rows, a.ld / std::gcd(a.ld, b.ld));
+    for (int64_t j = 0, at = d; j < rows && at < extent; ++j, at += b.ld) {
+        const int64_t row = at / a.ld, col = at % a.ld;
+        if (col < a.width || (col + b.width > a.ld && row + 1 < a.rows)) return true;
+    }
+    return false;
 }
 
-// Whether any of the first `outs` of `n` matrices overlaps another one of the n.
-inline bool overlap_any(const Rows *m, int outs, int n, int64_t rows) {
+// Whether any of the first `outs` of `n` overlaps another one of the n.
+inline bool overlap_any(const Rows *m, int outs, int n) {
     for (int i = 0; i < outs; ++i)
         for (int j = i + 1; j < n; ++j)
-            if (overlap(m[i], m[j], rows)) return true;
+            if (overlap(m[i], m[j])) return true;
     return false;
 }
 

@@ -109,8 +109,10 @@ extern "C" pact_status pact_rope(const pact_bf16 *x, int64_t ldx, int64_t M, int
     PACT_CHECK(ldx >= cols && ldy >= cols, PACT_ERR_SHAPE, "pact_rope: leading dimensions below heads * head_dim");
     PACT_CHECK(aligned16(x) && aligned16(y) && ldx % 8 == 0 && ldy % 8 == 0 && ((uintptr_t)positions & 3) == 0,
                PACT_ERR_ALIGN, "pact_rope: 16-byte aligned rows and 4-byte aligned positions needed");
-    PACT_CHECK((x == y && (ldx == ldy || M == 1)) || !overlap({x, ldx, cols}, {y, ldy, cols}, M), PACT_ERR_INVALID_ARG,
+    const Rows out = matrix(y, ldy, cols, M);
+    PACT_CHECK((x == y && (ldx == ldy || M == 1)) || !overlap(out, matrix(x, ldx, cols, M)), PACT_ERR_INVALID_ARG,
                "pact_rope: y overlaps x but is not x itself with its stride");
+    PACT_CHECK(!overlap(out, memory(positions, 4 * M)), PACT_ERR_INVALID_ARG, "pact_rope: y overlaps positions");
     rope::Turns turns = {};
     for (int i = 0; i < head_dim / 2; ++i) turns.per_pos[i] = inv_freq[i] * 0.15915494309189533577;   // 1 / (2 pi)
     const rope::Params p = {x, y, positions, ldx, ldy, M, heads, head_dim / 2, inverse != 0};

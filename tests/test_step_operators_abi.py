@@ -194,3 +194,48 @@ def test_an_update_over_its_inputs_is_refused(P, fp32):
         assert call(one, two, ws=one[o] - 16) == INVALID
     for i in ins:
         assert call(one, two, ws=two[i] - 16) == INVALID
+
+
+def test_statistics_and_scratch_over_other_memory_are_refused(P):
+    """lse and the workspace are outputs like the others, and no output may lie over the row numbers."""
+    lib = P.pact.lib
+    M, hq, freq = 300, 8, (ctypes.c_double * 64)()
+    at = {n: i << 20 for i, n in enumerate("q k v seq o lse dout dq dk dv ws".split(), 1)}
+    a = lambda: attention(P, q=at["q"], k=at["k"], v=at["v"], ldq=768, ldk=768, ldv=768, seq_start=at["seq"])
+    need = P.pact_attention_bwd_workspace_bytes(M, hq)
+
+    def bwd(**kw):
+        n = at | kw
+        g = P.pact.c_attention_grad(n["o"], 512, n["lse"], n["dout"], 512, n["dq"], 512, n["dk"], 128, n["dv"], 128)
+        return lib.pact_attention_bwd(a(), ctypes.byref(g), n["ws"], need, None)
+    width = {"q": 512, "k": 128, "v": 128}
+    for name in "qkv":
+        last = at[name] + 2 * (299 * 768 + width[name]) - 16    # the last 16 bytes of the last row
+        assert lib.pact_attention_fwd(a(), at["o"], 512, last, None) == INVALID and "overlap" in P.pact_last_error()
+        assert bwd(ws=last) == INVALID and "overlap" in P.pact_last_error()
+    assert lib.pact_attention_fwd(a(), at["o"], 512, at["o"] + 16, None) == INVALID
+    assert lib.pact_attention_fwd(a(), at["o"], 512, at["seq"] - 4 * M * hq + 16, None) == INVALID
+    assert lib.pact_attention_fwd(a(), at["seq"] - 16, 512, at["lse"], None) == INVALID
+    for name in ("o", "lse", "dout", "dq", "dk", "dv", "seq"):
+        assert bwd(ws=at[name] - need + 16) == INVALID and "overlap" in P.pact_last_error(), name
+    for name in ("dq", "dk", "dv"):
+        assert bwd(**{name: at["lse"]}) == bwd(**{name: at["seq"] - 16}) == INVALID
+    assert lib.pact_rope(at["q"], 512, 4, 4, 128, at["o"] + 16, freq, 0, at["o"], 512, None) == INVALID
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="accepted calls would launch on addresses of no memory")
+def test_overlaps_of_any_two_strides(P):
+    """Refused exactly where two matrices share an element, against their enumeration."""
+    import random
+    lib, freq, base, D = P.pact.lib, (ctypes.c_double * 32)(), 0x1000000, 64
+    rng = random.Random(5)
+    seen = [0, 0]
+    for _ in range(1500):
+        M, ldx, ldy = rng.randint(1, 7), 8 * rng.randint(8, 40), 8 * rng.randint(8, 40)
+        y = 8 * rng.randint(-7 * 40, 7 * 40)
+        cells = lambda p, ld: {p + r * ld + c for r in range(M) for c in range(D)}
+        share = bool(cells(0, ldx) & cells(y, ldy)) and not (y == 0 and (ldx == ldy or M == 1))
+        got = lib.pact_rope(base, ldx, M, 1, D, 0x2000, freq, 0, base + 2 * y, ldy, None)
+        assert (got == INVALID) == share, (M, ldx, ldy, y)
+        seen[share] += 1
+    assert min(seen) > 300
