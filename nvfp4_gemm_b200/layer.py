@@ -96,6 +96,8 @@ def check_packing(seq_start: torch.Tensor, sequences: int, M: int):
     """seq_start bounds `sequences` packed sequences of M rows."""
     if seq_start.dim() != 1 or seq_start.numel() != sequences + 1 or sequences < 1:
         raise ValueError(f"seq_start: shape {list(seq_start.shape)}, expected [{max(sequences, 1) + 1}]")
+    if seq_start.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"seq_start: {seq_start.dtype}, expected int32 row numbers")
     at = seq_start.tolist()
     if at != sorted(at) or at[0] < 0 or at[-1] > M:
         raise ValueError(f"seq_start: expected non-decreasing row numbers in [0, {M}]")
@@ -222,6 +224,7 @@ class PactLayer:
         self.heads, self.kv_heads = S.H // core.head_dim, S.KV // core.head_dim
         if self.heads % self.kv_heads:
             raise ValueError(f"{self.heads} query heads do not divide into {self.kv_heads} key heads")
+        check_packing(core.seq_start, core.seq_start.numel() - 1, S.M)   # before a cast could wrap or round it
         # host values, once: a device tensor's would be copied back by every call, and by none in a capture
         self.inv_freq = torch.as_tensor(core.inv_freq, dtype=torch.float64).cpu().contiguous()
         self.seq_start = core.seq_start.to(device=dev, dtype=torch.int32).clone()

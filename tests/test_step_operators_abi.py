@@ -239,3 +239,18 @@ def test_overlaps_of_any_two_strides(P):
         assert (got == INVALID) == share, (M, ldx, ldy, y)
         seen[share] += 1
     assert min(seen) > 300
+
+
+@pytest.mark.parametrize("starts,error", [([0, 2 ** 32, 2 ** 32 + 8], ValueError), ([0.0, 3.5, 8.0], TypeError),
+                                          ([False, True, True], TypeError)], ids=str)
+def test_a_packing_is_checked_before_it_is_cast(P, starts, error):
+    """Row numbers that an int32 would hold wrapped or rounded."""
+    from types import SimpleNamespace
+
+    from nvfp4_gemm_b200.layer import AttentionCore, LayerShape, PactLayer, check_packing
+    starts = torch.tensor(starts)
+    with pytest.raises(error):
+        check_packing(starts, 2, 10)
+    layer = SimpleNamespace(s=LayerShape(M=10, H=128, I=256, KV=64), attention=AttentionCore(64, starts, [0.0] * 32))
+    with pytest.raises(error):
+        PactLayer._init_attention(layer, "cpu")
