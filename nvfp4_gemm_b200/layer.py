@@ -96,7 +96,7 @@ def check_packing(seq_start: torch.Tensor, sequences: int, M: int):
     """seq_start bounds `sequences` packed sequences of M rows."""
     if seq_start.dim() != 1 or seq_start.numel() != sequences + 1 or sequences < 1:
         raise ValueError(f"seq_start: shape {list(seq_start.shape)}, expected [{max(sequences, 1) + 1}]")
-    if seq_start.dtype not in (torch.int32, torch.int64):
+    if seq_start.is_floating_point() or seq_start.is_complex() or seq_start.dtype == torch.bool:
         raise TypeError(f"seq_start: {seq_start.dtype}, expected int32 row numbers")
     at = seq_start.tolist()
     if at != sorted(at) or at[0] < 0 or at[-1] > M:

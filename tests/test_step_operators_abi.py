@@ -244,10 +244,11 @@ def test_overlaps_of_any_two_strides(P):
 @pytest.mark.parametrize("starts,error", [([0, 2 ** 32, 2 ** 32 + 8], ValueError), ([0.0, 3.5, 8.0], TypeError),
                                           ([False, True, True], TypeError)], ids=str)
 def test_a_packing_is_checked_before_it_is_cast(P, starts, error):
-    """Row numbers that an int32 would hold wrapped or rounded."""
+    """Row numbers that an int32 would hold wrapped or rounded; other whole numbers are as good as int32."""
     from types import SimpleNamespace
 
     from nvfp4_gemm_b200.layer import AttentionCore, LayerShape, PactLayer, check_packing
+    check_packing(torch.tensor([0, 3, 8], dtype=torch.int16), 2, 10)
     starts = torch.tensor(starts)
     with pytest.raises(error):
         check_packing(starts, 2, 10)
