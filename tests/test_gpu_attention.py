@@ -303,3 +303,15 @@ def test_a_query_that_is_not_finite_shows_in_its_gradients(D, lens, at):
     for name, t in (("dk", dk), ("dv", dv)):
         assert bool(t[a:row + 1, group].isnan().all()), name
         assert bool(t[:a].isfinite().all() and t[:, D:].isfinite().all()), name
+
+
+# Few rows under large groups: the gradients of k and v spread a key tile's heads over clusters of eight.
+GROUPS = [([1], 0, 24, 1, 128), ([130, 5], 0, 24, 1, 128), ([700], 0, 24, 1, 128), ([260, 0, 1], 9, 9, 1, 128),
+          ([127], 1, 16, 2, 128), ([400, 3], 0, 8, 1, 128), ([1], 0, 32, 1, 64), ([130, 5], 3, 32, 1, 64),
+          ([513], 0, 9, 1, 64), ([90] * 40, 0, 8, 1, 64)]
+
+
+@pytest.mark.parametrize("lens,pad,hq,hk,D", GROUPS, ids=[f"{len(c[0])}seq-{sum(c[0])}-h{c[2]}k{c[3]}d{c[4]}" for c in GROUPS])
+def test_large_groups(guards, lens, pad, hq, hk, D):
+    test_forward(guards, lens, pad, hq, hk, D)
+    test_gradient(guards, lens, pad, hq, hk, D)
