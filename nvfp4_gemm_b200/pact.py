@@ -166,6 +166,27 @@ def _stream(stream, dev: Optional[int] = None) -> Optional[int]:
     return int(stream)
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream`, from that stream's own pool: the current stream's may hand out a block
+    that work still pending there reads or writes."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):   # a raw handle; 0 and 1 are the default stream's
+        stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
+                  else torch.cuda.ExternalStream(int(stream), device=device))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output a call on `stream` allocates.  The current stream will read it, so the allocator is told: once
+    freed, it is not handed out again before that stream is through with it."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -193,9 +214,9 @@ class NVFP4Tensor:
     cols: int
 
     @staticmethod
-    def empty(rows: int, cols: int, device="cuda") -> "NVFP4Tensor":
-        codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=device)
-        scales = torch.empty(int(_lib.pact_scale_bytes(rows, cols)), dtype=torch.uint8, device=device)
+    def empty(rows: int, cols: int, device="cuda", stream=None) -> "NVFP4Tensor":
+        codes = _new((rows, cols // 2), torch.uint8, device, stream)
+        scales = _new(int(_lib.pact_scale_bytes(rows, cols)), torch.uint8, device, stream)
         return NVFP4Tensor(codes, scales, rows, cols)
 
     def c(self) -> c_nvfp4:
@@ -257,7 +278,7 @@ def pact_weight_cache_bytes(N: int, K: int) -> int:
 def pact_quantize_nvfp4(x: torch.Tensor, out: Optional[NVFP4Tensor] = None, stream=None) -> NVFP4Tensor:
     _bf16(x, "x")
     rows, cols = x.shape
-    out = out or NVFP4Tensor.empty(rows, cols, x.device)
+    out = out or NVFP4Tensor.empty(rows, cols, x.device, stream)
     s = out.c()
     _check(_lib.pact_quantize_nvfp4(x.data_ptr(), _ld(x), rows, cols, ctypes.byref(s), _stream(stream)))
     return out
@@ -268,11 +289,11 @@ def pact_rmsnorm_quant(x: torch.Tensor, gamma: torch.Tensor, eps: float, yq: Opt
                        want_y: bool = True, want_rstd: bool = True, stream=None):
     _bf16(x, "x")
     M, H = x.shape
-    yq = yq or NVFP4Tensor.empty(M, H, x.device)
+    yq = yq or NVFP4Tensor.empty(M, H, x.device, stream)
     if y is None and want_y:
-        y = torch.empty((M, H), dtype=torch.bfloat16, device=x.device)
+        y = _new((M, H), torch.bfloat16, x.device, stream)
     if rstd is None and want_rstd:
-        rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+        rstd = _new(M, torch.float32, x.device, stream)
     s = yq.c()
     _check(_lib.pact_rmsnorm_quant(x.data_ptr(), _ld(x), gamma.data_ptr(), float(eps), M, H, ctypes.byref(s),
                                    _ptr(y), _ptr(rstd), _stream(stream)))
@@ -289,11 +310,11 @@ def pact_silu_mul_quant(g: torch.Tensor, u: torch.Tensor, m: Optional[torch.Tens
         raise ValueError("g and u must share a row stride")
     M, I = g.shape
     if m is None and want_m:
-        m = torch.empty((M, I), dtype=torch.bfloat16, device=g.device)
-    mq = mq or NVFP4Tensor.empty(M, I, g.device)
+        m = _new((M, I), torch.bfloat16, g.device, stream)
+    mq = mq or NVFP4Tensor.empty(M, I, g.device, stream)
     if want_copies:
-        gq = gq or NVFP4Tensor.empty(M, I, g.device)
-        uq = uq or NVFP4Tensor.empty(M, I, g.device)
+        gq = gq or NVFP4Tensor.empty(M, I, g.device, stream)
+        uq = uq or NVFP4Tensor.empty(M, I, g.device, stream)
     smq, sgq, suq = mq.c(), gq.c() if gq else None, uq.c() if uq else None
     _check(_lib.pact_silu_mul_quant(g.data_ptr(), u.data_ptr(), _ld(g), M, I, _ptr(m), ctypes.byref(smq),
                                     ctypes.byref(sgq) if sgq else None, ctypes.byref(suq) if suq else None,
@@ -305,7 +326,7 @@ def pact_absmax_bf16(x: torch.Tensor, out: Optional[torch.Tensor] = None, stream
     """max |x| of a 2-D BF16 tensor, as a one-element FP32 device tensor."""
     _bf16(x, "x")
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=x.device)
+        out = _new(1, torch.float32, x.device, stream)
     _check(_lib.pact_absmax_bf16(x.data_ptr(), _ld(x), x.shape[0], x.shape[1], out.data_ptr(), _stream(stream)))
     return out
 
@@ -321,7 +342,7 @@ def pact_weight_layout_cache(W: torch.Tensor, stream=None, two_level: bool = Fal
     _bf16(W, "W")
     N, K = W.shape
     nbytes = pact_weight_cache_bytes(N, K)
-    buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=W.device)
+    buf = _new(nbytes + 256, torch.uint8, W.device, stream)
     off = (-buf.data_ptr()) % 256
     buf = buf[off:off + nbytes]
     c = c_weight_cache()
@@ -350,10 +371,10 @@ def pact_gptq_nvfp4(W: torch.Tensor, X: torch.Tensor, damp: float = 0.01, out: O
     _bf16(X, "X")
     N, K = W.shape
     n = X.shape[0]
-    out = out or NVFP4Tensor.empty(N, K, W.device)
+    out = out or NVFP4Tensor.empty(N, K, W.device, stream)
     need = pact_gptq_workspace_bytes(N, K, n)
     if workspace is None:
-        raw = torch.empty(need + 256, dtype=torch.uint8, device=W.device)
+        raw = _empty(need + 256, torch.uint8, W.device, stream)
         off = (-raw.data_ptr()) % 256
         workspace = raw[off:off + need]
     s = out.c()
@@ -368,7 +389,7 @@ def pact_weight_layout_cache_from_nvfp4(wf: NVFP4Tensor, gexp: int = 0, stream=N
     GPTQ-calibrated one)."""
     N, K = wf.rows, wf.cols
     nbytes = pact_weight_cache_bytes(N, K)
-    buf = torch.empty(nbytes + 256, dtype=torch.uint8, device=wf.codes.device)
+    buf = _new(nbytes + 256, torch.uint8, wf.codes.device, stream)
     off = (-buf.data_ptr()) % 256
     buf = buf[off:off + nbytes]
     c = c_weight_cache()
@@ -382,7 +403,7 @@ def pact_frozen_gemm_fwd(xq: NVFP4Tensor, w: WeightCache, lora: Optional[c_lora]
                          residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
                          stream=None) -> torch.Tensor:
     if y is None:
-        y = torch.empty((xq.rows, w.N), dtype=torch.bfloat16, device=xq.codes.device)
+        y = _new((xq.rows, w.N), torch.bfloat16, xq.codes.device, stream)
     s = xq.c()
     _check(_lib.pact_frozen_gemm_fwd(ctypes.byref(s), ctypes.byref(w.cstruct),
                                      ctypes.byref(lora) if lora is not None else None,
@@ -397,7 +418,7 @@ def pact_frozen_gemm_fwd_quant(xq: NVFP4Tensor, w: WeightCache, yq: Sequence[NVF
     """pact_frozen_gemm_fwd that also writes the NVFP4 copy of y, split along the
     columns into the tensors of yq (1 or 2, in column order)."""
     if y is None:
-        y = torch.empty((xq.rows, w.N), dtype=torch.bfloat16, device=xq.codes.device)
+        y = _new((xq.rows, w.N), torch.bfloat16, xq.codes.device, stream)
     s = xq.c()
     arr = (c_nvfp4 * len(yq))(*[t.c() for t in yq])
     _check(_lib.pact_frozen_gemm_fwd_quant(ctypes.byref(s), ctypes.byref(w.cstruct),
@@ -422,7 +443,7 @@ def pact_frozen_gemm_dgrad(dyq: NVFP4Tensor, w: WeightCache, lora: Optional[c_lo
                            residual: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
                            stream=None) -> torch.Tensor:
     if dx is None:
-        dx = torch.empty((dyq.rows, w.K), dtype=torch.bfloat16, device=dyq.codes.device)
+        dx = _new((dyq.rows, w.K), torch.bfloat16, dyq.codes.device, stream)
     s = dyq.c()
     _check(_lib.pact_frozen_gemm_dgrad(ctypes.byref(s), ctypes.byref(w.cstruct),
                                        ctypes.byref(lora) if lora is not None else None,
@@ -431,9 +452,9 @@ def pact_frozen_gemm_dgrad(dyq: NVFP4Tensor, w: WeightCache, lora: Optional[c_lo
     return dx
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, device) -> torch.Tensor:
+def _workspace(ws: Optional[torch.Tensor], need: int, device, stream) -> torch.Tensor:
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        ws = _empty(need, torch.uint8, device, stream)
     return ws
 
 
@@ -451,8 +472,8 @@ def pact_lora_fwd(x: torch.Tensor, A: torch.Tensor, scale: float, T: Optional[to
     M, K = x.shape
     R = A.shape[0]
     if T is None:
-        T = torch.empty((M, 2 * R), dtype=torch.bfloat16, device=x.device)
-    ws = _workspace(workspace, pact_lora_fwd_workspace_bytes(M, K, R), x.device)
+        T = _new((M, 2 * R), torch.bfloat16, x.device, stream)
+    ws = _workspace(workspace, pact_lora_fwd_workspace_bytes(M, K, R), x.device, stream)
     if xq is None:
         _check(_lib.pact_lora_fwd(x.data_ptr(), _ld(x), M, K, A.data_ptr(), R, float(scale), T.data_ptr(), _ld(T),
                                   ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -476,8 +497,8 @@ def pact_lora_fwd_silu(g: torch.Tensor, u: torch.Tensor, A: torch.Tensor, scale:
     M, I = g.shape
     R = A.shape[0]
     if T is None:
-        T = torch.empty((M, 2 * R), dtype=torch.bfloat16, device=g.device)
-    ws = _workspace(workspace, pact_lora_fwd_workspace_bytes(M, I, R), g.device)
+        T = _new((M, 2 * R), torch.bfloat16, g.device, stream)
+    ws = _workspace(workspace, pact_lora_fwd_workspace_bytes(M, I, R), g.device, stream)
     sq = mq.c()
     _check(_lib.pact_lora_fwd_silu(g.data_ptr(), u.data_ptr(), _ld(g), M, I, A.data_ptr(), R, float(scale),
                                    T.data_ptr(), _ld(T), ctypes.byref(sq), _ptr(m), _ld(m) if m is not None else 0,
@@ -498,7 +519,7 @@ def pact_lora_fwd_noalloc(x: torch.Tensor, A: torch.Tensor, scale: float, T: Opt
     M, K = x.shape
     R = A.shape[0]
     if T is None:
-        T = torch.empty((M, 2 * R), dtype=torch.bfloat16, device=x.device)
+        T = _new((M, 2 * R), torch.bfloat16, x.device, stream)
     _check(_lib.pact_lora_fwd_noalloc(x.data_ptr(), _ld(x), M, K, A.data_ptr(), R, float(scale), T.data_ptr(), _ld(T),
                                       _stream(stream)))
     return T
@@ -516,9 +537,9 @@ def pact_lora_bwd_u(dy: torch.Tensor, B: torch.Tensor, r: int, seg_end: Sequence
     _bf16(dy, "dy")
     M, N = dy.shape
     if U is None:
-        U = torch.empty((M, 2 * r * len(seg_end)), dtype=torch.bfloat16, device=dy.device)
+        U = _new((M, 2 * r * len(seg_end)), torch.bfloat16, dy.device, stream)
     se = (ctypes.c_int64 * 4)(*(list(seg_end) + [0] * (4 - len(seg_end))))
-    ws = _workspace(workspace, pact_lora_bwd_u_workspace_bytes(M, N, r, len(seg_end)), dy.device)
+    ws = _workspace(workspace, pact_lora_bwd_u_workspace_bytes(M, N, r, len(seg_end)), dy.device, stream)
     if dyq is None:
         _check(_lib.pact_lora_bwd_u(dy.data_ptr(), _ld(dy), M, N, B.data_ptr(), r, len(seg_end), se, float(scale),
                                     U.data_ptr(), _ld(U), ws.data_ptr(), ws.numel(), _stream(stream)))
@@ -556,14 +577,14 @@ def pact_lora_bwd(dy: torch.Tensor, A: torch.Tensor, U: torch.Tensor, r: int, se
     nseg = len(seg_end)
     gdt = torch.float32 if grads_fp32 else torch.bfloat16
     if dA is None:
-        dA = torch.empty((nseg * r, K), dtype=gdt, device=dy.device)
+        dA = _new((nseg * r, K), gdt, dy.device, stream)
     if dB is None:
-        dB = torch.empty((N, r), dtype=gdt, device=dy.device)
+        dB = _new((N, r), gdt, dy.device, stream)
     if dA.dtype != gdt or dB.dtype != gdt:
         raise TypeError(f"dA and dB must be {gdt}")
     need = pact_lora_bwd_workspace_bytes(M, N, K, r, nseg)
     if workspace is None:
-        workspace = torch.empty(need + 256, dtype=torch.uint8, device=dy.device)
+        workspace = _empty(need + 256, torch.uint8, dy.device, stream)
         off = (-workspace.data_ptr()) % 256
         workspace = workspace[off:off + need]
     xq_s = xq.c() if xq is not None else None
@@ -589,7 +610,7 @@ def pact_round_bf16(x: torch.Tensor, y: Optional[torch.Tensor] = None, stream=No
     if x.dtype != torch.float32 or not x.is_contiguous():
         raise TypeError("x: expected a contiguous float32 tensor")
     if y is None:
-        y = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        y = _new(x.shape, torch.bfloat16, x.device, stream)
     _check(_lib.pact_round_bf16(x.data_ptr(), y.data_ptr(), x.numel(), _stream(stream)))
     return y
 
@@ -600,10 +621,10 @@ def pact_silu_mul_bwd_quant(dm: torch.Tensor, gq: NVFP4Tensor, uq: NVFP4Tensor, 
     _bf16(dm, "dm")
     M, I = dm.shape
     if dgu is None:
-        dgu = torch.empty((M, 2 * I), dtype=torch.bfloat16, device=dm.device)
-    dguq = dguq or NVFP4Tensor.empty(M, 2 * I, dm.device)
+        dgu = _new((M, 2 * I), torch.bfloat16, dm.device, stream)
+    dguq = dguq or NVFP4Tensor.empty(M, 2 * I, dm.device, stream)
     if m_re is None and want_m:
-        m_re = torch.empty((M, I), dtype=torch.bfloat16, device=dm.device)
+        m_re = _new((M, I), torch.bfloat16, dm.device, stream)
     sg, su, sd = gq.c(), uq.c(), dguq.c()
     _check(_lib.pact_silu_mul_bwd_quant(dm.data_ptr(), _ld(dm), ctypes.byref(sg), ctypes.byref(su), M, I,
                                         dgu.data_ptr(), _ld(dgu), ctypes.byref(sd), _ptr(m_re), _stream(stream)))
@@ -616,9 +637,9 @@ def pact_rmsnorm_bwd(dy: torch.Tensor, yq: NVFP4Tensor, rstd: torch.Tensor, gamm
     _bf16(dy, "dy")
     M, H = dy.shape
     if dx is None:
-        dx = torch.empty((M, H), dtype=torch.bfloat16, device=dy.device)
+        dx = _new((M, H), torch.bfloat16, dy.device, stream)
     if dxq is None and want_q:
-        dxq = NVFP4Tensor.empty(M, H, dy.device)
+        dxq = NVFP4Tensor.empty(M, H, dy.device, stream)
     sy = yq.c()
     sq = dxq.c() if dxq is not None else None
     _check(_lib.pact_rmsnorm_bwd(dy.data_ptr(), _ld(dy), ctypes.byref(sy), rstd.data_ptr(), gamma.data_ptr(), M, H,
@@ -661,27 +682,6 @@ def _matrix(t: torch.Tensor, name: str, dev: int, shape=None) -> int:
         raise ValueError(f"{name}: expected a matrix with contiguous rows")
     # a single row's stride is arbitrary in PyTorch: any legal one serves
     return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """Memory for a call on `stream`, from that stream's own pool: the current stream's may hand out a block
-    that work still pending there reads or writes."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):   # a raw handle; 0 and 1 are the default stream's
-        stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
-                  else torch.cuda.ExternalStream(int(stream), device=device))
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output a call on `stream` allocates.  The caller's stream will read it, so the allocator is told: once
-    freed, it is not handed out again before that stream is through with it."""
-    t = _empty(shape, dtype, device, stream)
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream())
-    return t
 
 
 def _scratch(ws: Optional[torch.Tensor], need, device, dev: int, stream) -> torch.Tensor:
