@@ -455,7 +455,10 @@ PACT_API pact_status pact_rope(const pact_bf16 *x, int64_t ldx, int64_t M, int h
  * h reads key head h / (heads / kv_heads).  For row i of a sequence, over its rows j <= i:
  *   S_ij = scale q_i . k_j,  lse_i = log sum_j exp S_ij,  o_i = sum_j exp(S_ij - lse_i) v_j
  * Scores, softmax statistics and sums are FP32; the probabilities enter the second
- * product as BF16 (as q, k and v do), o is rounded once to BF16. */
+ * product as BF16 (as q, k and v do), o is rounded once to BF16.  Scores may reach 2^30 in
+ * magnitude: beyond, their roundings exceed the exponents that FP32 has, and a row may come
+ * out as NaN.  Matrices need 16-byte aligned rows (pointers, and strides that are multiples of
+ * 8), lse a 16-byte aligned pointer. */
 typedef struct {
     int64_t M;                 /* rows of q, k, v and the outputs (1 .. 2^30) */
     int heads, kv_heads;       /* heads a multiple of kv_heads */
@@ -487,9 +490,11 @@ PACT_API pact_status pact_attention_fwd(const pact_attention_t *a, pact_bf16 *o,
  *   dq_i = scale sum_j dS_ij k_j;  dk_j = scale sum dS_ij q_i,  dv_j = sum P_ij do_i  over
  *   the rows i and the query heads of j's group.
  * P and dS enter their products as BF16; every sum is FP32 in a fixed order (repeated
- * calls agree bit for bit).  Rows of no sequence are left as they were; outputs and a
- * workspace that overlap one another or an input are refused.  workspace (device, 16-byte aligned,
- * >= pact_attention_bwd_workspace_bytes(M, heads)) is scratch; calls that share it must not
+ * calls agree bit for bit).  P is formed from lse as the forward left it, in FP32, so its
+ * relative error grows with the scores: 2^-23 |lse|, that of a BF16 rounding at some 30000.
+ * Rows of no sequence are left as they were; outputs and a workspace that overlap one another
+ * or an input are refused.  workspace (device, 16-byte aligned, >=
+ * pact_attention_bwd_workspace_bytes(M, heads)) is scratch; calls that share it must not
  * overlap on the GPU. */
 typedef struct {
     const pact_bf16 *o;        /* [M x heads*head_dim] as written by the forward */
@@ -519,7 +524,9 @@ PACT_API pact_status pact_attention_bwd(const pact_attention_t *a, const pact_at
  * m and W are FP32 (a BF16 weight would lose small steps); W' is also written rounded
  * to BF16 where weight_bf16 is not NULL, the adapter the LoRA products read.  Gradients
  * are BF16, or FP32 when grad_fp32 != 0 (pact_lora_bwd's two forms).  The r x r products
- * run in FP64. */
+ * run in FP64.  lr, momentum and weight_decay are values: a captured call keeps those it was
+ * captured with.  A call's largest rank sets the kernels that all its matrices take, so ranks above
+ * 48 are better off in a call of their own. */
 typedef struct {
     const void *grad;          /* [count x rows x cols], contiguous, as are all below */
     const float *momentum;     /* m */

@@ -193,8 +193,9 @@ __device__ __forceinline__ void clear_rows(uint8_t *tile, int row, int lane) {
 }
 
 // N accumulator columns (from `taddr`) of a warp's 32 lanes, each times its lane's f, as BF16 to the rows of
-// dst (leading dimension ld, first column already added), rows from `rows` on left out.  A lane holds a row, so the values pass through 4 KiB of shared memory (16-byte chunk
-// c of row r at c ^ (r % 8)): stores of whole 128-byte lines, four rows an instruction.
+// dst (leading dimension ld, first column already added), rows from `rows` on left out.  A lane holds
+// a row, so the values pass through 4 KiB of shared memory (16-byte chunk c of row r at
+// c ^ (r % 8)): stores of whole 128-byte lines, four rows an instruction.
 // Stored straight from the lanes, 32 rows an instruction, a tile took 4.4 us; this way 1.
 template <int N>
 __device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t *slab, pact_bf16 *dst, int64_t ld,
@@ -238,11 +239,13 @@ __device__ __forceinline__ void store_rows(uint32_t taddr, float f, uint8_t *sla
 // The order of work.  Each sequence is cut into tiles of 1 << shift rows, and a tile's work grows with its
 // place in the sequence (query tiles: later queries see more keys) or with the tiles behind it (key
 // tiles).  Long work goes first, or a long sequence at the wrong end of a ragged batch keeps a
-// few SMs busy when the others are done (8061 tokens in sequences of 1 to 2900, forward: 76 us
-// in the order of the batch, 64 sorted).  Query tiles are sorted by their place over all
+// few SMs busy when the others are done (8061 tokens in eight sequences of 1 to 2900, 12 and 2
+// heads of 128, cold L2: forward 82 us in the order of the batch, 68 sorted, gradients 224 and
+// 210).  Sorted are up to 32 sequences, one to a lane; more come in the order of the batch
+// and pay that difference where they are as uneven.  Query tiles are sorted by their place over all
 // sequences; key tiles one sequence after the other, the longest first, because all of a
 // sequence's key tiles read its queries and output gradients, which then stay in L2 (gradients
-// over 4 x 2048 tokens: 348 us, 360 sorted by place).
+// over 4 x 2048 tokens: 3% faster than sorted by place).
 struct Tiles {
     int shift;    // 128 or 256 rows
     int pairs;    // pairs of units per tile (below)
@@ -393,16 +396,21 @@ static_assert(2 * 128 * 216 + 128 * 72 <= SPLIT_THREADS * 168, "more registers t
 //                    its first 64 keys while the rest is computed.
 //   warp 8           the plan, and TMA: the two Q tiles, then K and V tiles through a ring
 //   warp 9           the MMAs, in the order  P0 V(j), S0(j+1), P1 V(j), S1(j+1)
-// The accumulator is rescaled only when a row's maximum grew by more than 2^8 since the
-// last time (any factor cancels in O / l; FP32 has the room), which is rare after the
-// first block.  S(j+1) is issued behind P V(j), so a unit that sees its scores ready
+// The running maximum and sum are those of the online softmax (Milakov and Gimelshein, 2018).  The
+// accumulator is rescaled only when a row's maximum grew by more than 2^8 since the last time
+// (any factor cancels in O / l; FP32 has the room), which is rare after the first block; this, and
+// exponentials on the FP32 units in the gradients, are published for attention on this
+// generation of GPUs.  S(j+1) is issued behind P V(j), so a unit that sees its scores ready
 // also knows its accumulator at rest.  The CTA is persistent: the next pair's Q, K and scores
 // come under the last pair's output.
 // Rounding: P to BF16, as the MMA takes it (by at most 2^-8 of a probability); the row sums add the FP32 values.
-// 4 x 2048 tokens, 24 and 8 heads of 128: 118 us, 871 TFLOP/s of the 103 GFLOP under the diagonal (52% of
-// the measured BF16 rate).  A block of a pair takes 3000 cycles for 2048 of MMAs: a unit's softmax takes
-// 1500 (1024 of them the special-function units'), and with two units in tensor memory it is not
-// wholly under the other's products.  Tried without gain: sixteen softmax warps, two threads a row that
+// 4 x 2048 tokens, 24 and 8 heads of 128: 118 to 122 us, some 860 TFLOP/s of the 103 GFLOP under the
+// diagonal (52% of the measured BF16 rate); 32 and 8 heads of 64: 131 us, 524 TFLOP/s.  At D = 128 a block of a
+// pair takes 3000 cycles for 2048 of MMAs: a unit's softmax takes 1500 (1024 of them the
+// special-function units'), and with two units in tensor memory it is not wholly under the other's
+// products.  Those blocks, 45 an SM, are 71% of the cycles that an SM is active (the tensor pipe is
+// active in 48%); the rest is what comes once a pair: its first loads and scores, the mask of the diagonal
+// block, the output.  It has not been taken apart.  Tried without gain: sixteen softmax warps, two threads a row that
 // exchange their maxima (3% slower), and with them a share of the exponentials on the FP32 units (more so).
 namespace fwd {
 constexpr int STAGES = 4;
@@ -693,8 +701,11 @@ k_attn_fwd(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // This kernel also leaves delta and lse log2(e) for the other one, which is launched while this one
 // runs, loads its first tiles and waits with those two alone (some 2 us a call).
 // Rounding: dS to BF16, as the MMA takes it; P, dP and the sums stay FP32.
-// 4 x 2048 tokens, 24 and 8 heads of 128: some 185 us (three products: 37% of the measured BF16 rate).  A
-// block of a pair takes 4700 cycles for 48 MMAs of 64; the tensor core waits for dS, 1400 cycles after dP.
+// 4 x 2048 tokens, 24 and 8 heads of 128, alone with a cold L2: 190 us (three products, 155 GFLOP: 49% of the
+// measured BF16 rate).  A block of a pair takes 4700 cycles for 48 MMAs of 64; the tensor core waits for
+// dS, 1400 cycles after dP.  The blocks are 71% of an SM's active cycles; the rest is what a CTA does once
+// (set-up, first tiles, delta, output), five CTAs an SM one after the other.  P beside dP exceeds the 104
+// registers a thread: 52 bytes are spilled and 68 read back a block at D = 128, 32 and 48 at D = 64.
 // Tried without gain: persistent CTAs (V's memory is needed to pass the output on), MMA waits
 // moved ahead, dO for delta from its tile.
 // The gradient kernels' softmax needs no exchange between the columns of a row (lse is known), so
@@ -993,7 +1004,8 @@ k_attn_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 //   dV(n) S(n+1) | dK(n) dP(n+1): the exponentials of n+1 run under the second pair.
 // Four warpgroups share the columns: warps 4 w .. 4 w + 3 take queries 16 w .. 16 w + 15 of both halves of a tile.
 // Rounding: P and dS to BF16, as the MMA takes them.
-// 4 x 2048 tokens, 24 and 8 heads of 128: some 175 us (four products: 49% of the measured BF16 rate).  A
+// 4 x 2048 tokens, 24 and 8 heads of 128, alone with a cold L2: 186 us (four products, 206 GFLOP: 67% of the
+// measured BF16 rate); with dq's kernel 380 to 400 a call.  The units are 80% of an SM's active cycles.  A
 // unit takes 2530 cycles for 2048 of MMAs: P (1220, of them 900 the special-function units') and dV, S(n+1)
 // behind it follow one another, as D = 128 leaves no tensor memory for a second S.  A second S at D = 64
 // and a third Q slot changed nothing (P and dS then follow one another without a gap, in the same time).
@@ -1402,9 +1414,10 @@ static pact_status run_bwd(const Params &p, cudaStream_t st) {
     if (s != PACT_OK) return s;
     // A key tile's CTA runs over all later query tiles of the group's heads.  Where there are fewer key
     // tiles than SMs, the heads are spread over a cluster of CTAs that add their sums at the end,
-    // for some 5 us.  Gradients over 1999 tokens, 32 and 8 heads of 64 (128 tiles): 137 us with one
-    // CTA a tile, 106 with two, 136 with four; 2048 tokens, 12 and 2 heads of 128 (32 tiles): 193, 128,
-    // 107; 8192 tokens, 24 and 8 heads of 128 (512 tiles): 343, 446 with two.
+    // for some 5 us.  Gradients (cold L2) over 2048 tokens, 12 and 2 heads of 128 (32 tiles): 202 us with one CTA
+    // a tile, 142 with two, 124 with four; 1999 tokens, 32 and 8 heads of 64 (128 tiles): 118, 101, 132; 8192
+    // tokens, 24 and 8 heads of 128 (512 tiles): 380, 492 with two.  The rule sees tiles, not the lengths
+    // that make them: four sequences of 512, 32 and 8 heads of 64 (128 tiles again, but short): 62, 69, 91.
     const int group = p.heads / p.kv_heads;
     int ns = 1;
     while (2 * ns <= group && ns < 8 && ns * (int64_t)(p.M / TILE + 1) * p.kv_heads < sm_count()) ns *= 2;

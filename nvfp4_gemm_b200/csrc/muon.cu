@@ -19,7 +19,12 @@
 // CTAs of an SM: the 392 adapter matrices of 28 layers (rank 16, 406 MB) take 126 us, 3.2 TB/s or
 // 49% of the measured copy rate, the 14 of one layer 18.  Tried: whole float4s of u through shared memory
 // (4% slower), clusters of sixteen with three or four CTAs an SM (10 to 30% slower), a later CTA's g and m
-// asked into L2 ahead of it (3% faster, not worth its code).  Larger ones take three kernels:
+// asked into L2 ahead of it (3% faster, not worth its code).  Larger ones take three kernels.
+// The largest rank of a call sets the block size of all its matrices, and beyond 48 all of them take
+// the three kernels: one matrix of 64 x 64 beside those 392 makes 1374 us of 132 (cold L2).  One that
+// needs more shared memory than two CTAs have room for on an SM leaves one an SM to every matrix of its
+// launch: one of 16 x 14000 beside them, 198 us.  The 14 matrices of one layer at rank 48: 129 us, at
+// rank 64: 159 (rank 16: 28).  The three kernels:
 //   k_muon_gram   a slab of the long side per CTA: m' is written, the slab's part of
 //                 u u^T goes to scratch
 //   k_muon_poly   one CTA per matrix: S0 from the parts in a fixed order, then P

@@ -276,7 +276,8 @@ class PactLayer:
 
     def update(self, lr: float, momentum: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True):
         """One step of the adapters from the gradients the backward left (the FP32 ones
-        with grad_fp32): the masters, their BF16 copies the products read, the momenta."""
+        with grad_fp32): the masters, their BF16 copies the products read, the momenta.  A captured
+        update keeps the lr, momentum and weight_decay it was captured with."""
         if not self.trainable:
             raise RuntimeError("update() needs PactLayer(..., trainable=True)")
         P.pact_muon_step(self._matrices(self.masters), self._matrices(self.grads32 if self.grad_fp32 else self.grads),

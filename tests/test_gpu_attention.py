@@ -315,3 +315,23 @@ GROUPS = [([1], 0, 24, 1, 128), ([130, 5], 0, 24, 1, 128), ([700], 0, 24, 1, 128
 def test_large_groups(guards, lens, pad, hq, hk, D):
     test_forward(guards, lens, pad, hq, hk, D)
     test_gradient(guards, lens, pad, hq, hk, D)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_scores_up_to_the_documented_size(D):
+    """Scores of some 2^29, all apart by far more than an exponent: each row is its best key's v, off by the
+    roundings of P and of o, and its log-sum that key's score."""
+    import nvfp4_gemm_b200 as P
+    n, size = 300, 2.0 ** 15
+    g = torch.Generator(device="cuda").manual_seed(9)
+    weight = (torch.randperm(256, generator=g, device="cuda")[torch.arange(n, device="cuda") % 256] - 128).double() / 128
+    q, k = (torch.zeros((n, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q[:, 0], k[:, 0] = size, (weight * size / 2).bfloat16()
+    v = bf(10, n, D)
+    cu = torch.tensor([0, 256], dtype=torch.int32, device="cuda")     # one key of each weight
+    o, lse = P.pact_attention_fwd(q, k, v, cu, 1, 1, scale=1.0)
+    status_ok()
+    best = torch.cummax(k[:256, 0].double(), 0)
+    want = v[:256].double()[best.indices]
+    assert bool(((o[:256].double() - want).abs() <= 2.1 * ref64.H * want.abs() + ref64.T).all())
+    assert bool(((lse[0, :256].double() - best.values * size).abs() <= 4 * ref64.U * best.values.abs() * size + 1).all())
