@@ -183,7 +183,7 @@ def _new(shape, dtype, device, stream) -> torch.Tensor:
     freed, it is not handed out again before that stream is through with it."""
     t = _empty(shape, dtype, device, stream)
     if stream is not None:
-        t.record_stream(torch.cuda.current_stream())
+        t.record_stream(torch.cuda.current_stream(t.device))
     return t
 
 

@@ -335,3 +335,32 @@ def test_scores_up_to_the_documented_size(D):
     want = v[:256].double()[best.indices]
     assert bool(((o[:256].double() - want).abs() <= 2.1 * ref64.H * want.abs() + ref64.T).all())
     assert bool(((lse[0, :256].double() - best.values * size).abs() <= 4 * ref64.U * best.values.abs() * size + 1).all())
+
+
+@pytest.mark.parametrize("at", [0, 1, 17, 130])
+@pytest.mark.parametrize("which", ["k", "v", "do"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_values_and_output_gradients_that_are_not_finite_show(D, which, at):
+    """A NaN enters every result that the formula takes it into, and no other sequence's."""
+    import nvfp4_gemm_b200 as P
+    lens, hq, hk, head, col = [40, 200], 4, 2, 2, 5     # heads 2 and 3 read key head 1
+    q, k, v, cu, starts, M = problem(lens, 0, hq, hk, D)
+    do = bf(2, M, hq * D)
+    a, group = lens[0], slice(D, 2 * D)
+    {"k": k[:, group], "v": v[:, group], "do": do[:, head * D:(head + 1) * D]}[which][a + at, col] = math.nan
+    o, lse = P.pact_attention_fwd(q, k, v, cu, hq, hk)
+    dq, dk, dv = P.pact_attention_bwd(do, q, k, v, o, lse, cu, hq, hk)
+    status_ok()
+    nan = lambda t: bool(t.isnan().all())
+    own = slice(head * D, (head + 1) * D)
+    later, seen = slice(a + at, M), slice(a, a + at + 1)     # rows that see key `at`; keys that row `at` sees
+    if which == "k":
+        assert nan(lse[head, later]) and nan(o[later, own]) and nan(dq[later, own])
+        assert nan(dk[a:, group]) and nan(dv[a:, group])     # the last row, of no log-sum, sees them all
+    elif which == "v":
+        assert nan(o[later, own][:, col]) and nan(dq[later, own]) and nan(dk[a:, group])
+        assert bool(lse.isfinite().all())
+    else:
+        assert nan(dq[a + at, own]) and nan(dk[seen, group]) and nan(dv[seen, group][:, col])
+    for t in (o, dq, dk, dv, lse.T):
+        assert bool(t[:a].isfinite().all())
