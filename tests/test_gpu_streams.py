@@ -82,3 +82,32 @@ def test_memory_of_the_calls_stream():
         if "layout_cache" not in name:
             assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, ref)), name
     assert P.pact_get_device_status() == 0, P.pact_last_error()
+
+
+def test_captured_on_a_second_stream():
+    """A fork of a captured step that gives its calls the second stream: their memory is the graph's."""
+    import nvfp4_gemm_b200 as P
+    g = torch.Generator(device="cuda").manual_seed(4)
+    hq, hk, D = 4, 2, 64
+    bf = lambda n: torch.randn((300, n), generator=g, device="cuda").bfloat16()
+    q, k, v, do = bf(hq * D), bf(hk * D), bf(hk * D), bf(hq * D)
+    cu = torch.tensor([0, 130, 300], dtype=torch.int32, device="cuda")
+
+    def step(stream):
+        o, lse = P.pact_attention_fwd(q, k, v, cu, hq, hk, stream=stream)
+        grads = P.pact_attention_bwd(do, q, k, v, o, lse, cu, hq, hk, stream=stream)
+        return [o, lse, *grads, *tensors(P.pact_quantize_nvfp4(grads[0], stream=stream))]
+    want = step(None)
+    torch.cuda.synchronize()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        got = step(side)
+        torch.cuda.current_stream().wait_stream(side)
+        copies = [t.clone() for t in got]
+    for _ in range(3):
+        other = [torch.full((1 << 20,), 3.0, device="cuda") for _ in range(4)]   # work beside the graph's memory
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) and torch.equal(c, b) for a, b, c in zip(got, want, copies))
+    assert all(bool((t == 3.0).all()) for t in other)
